@@ -86,6 +86,7 @@ typedef int mom_rule;
 #define MOM_DEVERR_ROW_INDEX  2  /* a row / token index outside its array */
 #define MOM_DEVERR_SEGMENT    3  /* segment bounds decreasing or beyond n_rows */
 #define MOM_DEVERR_TIMEOUT    4  /* a pipeline wait inside a kernel gave up (internal error) */
+#define MOM_DEVERR_TARGET     5  /* a target class >= vocab (mom_linear_ce_*; info: its row) */
 
 #define MOM_WS_HEADER_BYTES 256
 
@@ -766,6 +767,105 @@ mom_status mom_short_conv_bwd(const mom_conv_bwd_problem* problems, int n_proble
 /* mom_convert -- dst[i] = src[i] converted between float32 and bf16 (round
  * to nearest even), i < n. */
 mom_status mom_convert(const void* src, mom_dtype src_dt, void* dst, mom_dtype dst_dt, int64_t n, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Around the blocks in a training step: the residual stream with the norms
+ * before and after each block, 8-bit checkpoints of the activations that the
+ * backward pass needs again, and the vocabulary's cross entropy.
+ * In these calls a row may start at any element boundary; rows whose width
+ * is a multiple of 8 in 16-byte aligned arrays take 16-byte accesses.
+ * ---------------------------------------------------------------------- */
+
+/* 8-bit activation checkpoints: groups of MOM_ACT8_GROUP channels of a row
+ * (the last one may be shorter) share scale = float32(max|x| / 127); the codes
+ * are round_half_even(x / scale), exactly, and the restored value is code *
+ * scale (one rounding to float32, one more to bf16).  A group whose largest
+ * magnitude is below 2^-100 is stored as zeros; a group with an infinity or a
+ * NaN restores to NaN throughout. */
+#define MOM_ACT8_GROUP 128
+
+/* mom_act_pack8 -- x [n_rows, d] (dt) -> codes [n_rows, d] int8, scales
+ * [n_rows, ceil(d / MOM_ACT8_GROUP)] float32.  n_rows may be 0. */
+mom_status mom_act_pack8(const void* x, mom_dtype dt, int64_t n_rows, int d, int8_t* codes, float* scales,
+                         void* stream);
+/* mom_act_unpack8 -- the restored values, x [n_rows, d] (dt). */
+mom_status mom_act_unpack8(const int8_t* codes, const float* scales, int64_t n_rows, int d, void* x, mom_dtype dt,
+                           void* stream);
+
+typedef int mom_gate_mode;
+#define MOM_GATE_NONE    0
+#define MOM_GATE_TOKEN   1  /* gate [n_rows]: one logit a row */
+#define MOM_GATE_ELEMENT 2  /* gate [n_rows, d] */
+#define MOM_NORM_MAX_D   16384
+
+/* mom_residual_norm -- the residual stream past one block, and the norm
+ * before the next:
+ *   x_out = x + res_scale * sigmoid(gate) * (y / rms(y)) * w_post
+ *   h     = (x_out / rms(x_out)) * w_pre           rms(a) = sqrt(mean(a^2) + eps) over a row
+ * x, x_out [n_rows, d] in x_dt; y, gate and h in dt; w_post, res_scale, w_pre
+ * [d] float32.  (x_dt, dt) is (BF16, BF16), (F32, BF16) or (F32, F32).
+ *   x = NULL       the stream is restored from x_codes / x_scales (as
+ *                  mom_act_pack8 writes them); x_dt is then x_out's type
+ *   y = NULL       no block: x_out = x (gate_mode MOM_GATE_NONE, w_post,
+ *                  res_scale NULL); the norm before a first block, or the
+ *                  restore of a checkpoint with its norm
+ *   res_scale NULL 1
+ *   x_out, h       either may be NULL (h NULL: w_pre is not read)
+ *   codes_out, scales_out   NULL, or the 8-bit checkpoint of x (not of x_out),
+ *                  which must then be given as x
+ * h and the norms are formed from the float32 x_out, before it is rounded to
+ * x_dt.  x_out may be x, and h may be y; nothing else may overlap an output.
+ * d <= MOM_NORM_MAX_D (MOM_ERR_UNSUPPORTED). */
+mom_status mom_residual_norm(const void* x, const int8_t* x_codes, const float* x_scales, const void* y,
+                             const void* gate, mom_gate_mode gate_mode, const float* w_post, const float* res_scale,
+                             const float* w_pre, float eps, int64_t n_rows, int d, mom_dtype x_dt, mom_dtype dt,
+                             void* x_out, void* h, int8_t* codes_out, float* scales_out, void* stream);
+
+/* mom_residual_norm_bwd -- the adjoint at the same inputs, from dx_out (the
+ * gradient of x_out; NULL: 0) and dh (of h; NULL: no norm before a next
+ * block, w_pre is not read), both [n_rows, d] in g_dt:
+ *   dx [n_rows, d] (g_dt), dy [n_rows, d] and dgate [n_rows] or [n_rows, d]
+ *   (dt), dw_post, dres_scale, dw_pre [d] float32 (overwritten).
+ * dgate, dw_post, dres_scale and dw_pre may be NULL (not wanted); without y,
+ * dy, dgate, dw_post and dres_scale must be.  dx may be dx_out, dy may be y.
+ * Column sums are added in a fixed order (no atomics).  n_rows = 0 gives zero
+ * weight gradients.  ws: mom_residual_norm_bwd_workspace_size(). */
+size_t mom_residual_norm_bwd_workspace_size(int64_t n_rows, int d);
+mom_status mom_residual_norm_bwd(const void* x, const int8_t* x_codes, const float* x_scales, const void* y,
+                                 const void* gate, mom_gate_mode gate_mode, const float* w_post,
+                                 const float* res_scale, const float* w_pre, float eps, int64_t n_rows, int d,
+                                 mom_dtype x_dt, mom_dtype dt, const void* dx_out, const void* dh, mom_dtype g_dt,
+                                 void* dx, void* dy, void* dgate, float* dw_post, float* dres_scale, float* dw_pre,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/* mom_linear_ce_fwd -- softmax cross entropy of the logits z = x w^T, which
+ * are never stored: x [n_rows, d], w [vocab, d] (dt), targets [n_rows] int32;
+ *   lse[t]  = log(sum_v exp(z[t, v]))
+ *   loss[t] = lse[t] - z[t, targets[t]];  0 where targets[t] < 0 (padding)
+ *   mean[0] = sum of loss / rows with a target,  mean[1] = 1 / rows with a
+ *             target (both 0 when no row has one); mean may be NULL
+ * loss, lse [n_rows] float32.  A target >= vocab is recorded in ws
+ * (MOM_DEVERR_TARGET) and counts as padding.  x and w are 16-byte aligned; d
+ * and vocab may be any sizes.  Products are on the bf16 tensor cores with
+ * float32 accumulation; float32 operands are split into three bf16 parts.
+ * ws: mom_linear_ce_workspace_size(.., backward = 0). */
+size_t mom_linear_ce_workspace_size(int64_t n_rows, int d, int64_t vocab, mom_dtype dt, int backward);
+mom_status mom_linear_ce_fwd(const void* x, const void* w, const int32_t* targets, mom_dtype dt, int64_t n_rows,
+                             int d, int64_t vocab, float* loss, float* lse, float* mean, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* mom_linear_ce_bwd -- the gradient of sum_t r[t] loss[t], r[t] = dloss[t] *
+ * dscale[0] (either NULL: 1; with dscale = mean + 1 of the forward and dloss
+ * NULL, of the mean loss), from the forward's lse: with g[t, v] = r[t] (exp(z
+ * - lse) - [v = target]), 0 for padding rows,
+ *   dx = g w [n_rows, d],  dw = g^T x [vocab, d]   (dt, overwritten)
+ * The logits are formed again in pieces of the vocabulary and g is held for
+ * one piece at a time (rounded to bf16, three bf16 parts for float32).  dx,
+ * dw 16-byte aligned.  n_rows = 0 gives dw = 0.
+ * ws: mom_linear_ce_workspace_size(.., backward = 1). */
+mom_status mom_linear_ce_bwd(const void* x, const void* w, const int32_t* targets, const float* lse,
+                             const float* dloss, const float* dscale, mom_dtype dt, int64_t n_rows, int d,
+                             int64_t vocab, void* dx, void* dw, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

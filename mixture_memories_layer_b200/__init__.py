@@ -5,4 +5,4 @@ combine, recurrent decode) and a thin Python binding over it.
 Importing the package loads nothing; ``mixture_memories_layer_b200.binding``
 loads the shared library and fails loudly if it is missing.
 """
-__all__ = ["binding", "layer", "synth"]
+__all__ = ["binding", "layer", "block", "residual", "lm_head", "synth"]

@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmom_b200
 MOM_OK, MOM_ERR_ARG, MOM_ERR_UNSUPPORTED, MOM_ERR_CUDA, MOM_ERR_DEVICE = 0, 1, 2, 3, 4
 MOM_F32, MOM_BF16 = 0, 1
 MOM_DEVERR_NONE, MOM_DEVERR_MEM_INDEX, MOM_DEVERR_ROW_INDEX, MOM_DEVERR_SEGMENT, MOM_DEVERR_TIMEOUT = 0, 1, 2, 3, 4
+MOM_DEVERR_TARGET = 5
 MOM_WS_HEADER_BYTES = 256
 MOM_SELFTEST_WAIT_SITE = 990
 
@@ -93,6 +94,16 @@ SIGNATURES = {
                                    _VP, _VP, _SZ, _VP]),
     "mom_block_conv_state": (_I, [_VP, _VP, _VP, _VP, _VP, _I64, _I, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP, _VP, _SZ,
                                   _VP]),
+    "mom_act_pack8": (_I, [_VP, _I, _I64, _I, _VP, _VP, _VP]),
+    "mom_act_unpack8": (_I, [_VP, _VP, _I64, _I, _VP, _I, _VP]),
+    "mom_residual_norm": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _VP, _VP, _VP, _F, _I64, _I, _I, _I, _VP, _VP, _VP, _VP,
+                               _VP]),
+    "mom_residual_norm_bwd_workspace_size": (_SZ, [_I64, _I]),
+    "mom_residual_norm_bwd": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _VP, _VP, _VP, _F, _I64, _I, _I, _I, _VP, _VP, _I,
+                                   _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "mom_linear_ce_workspace_size": (_SZ, [_I64, _I, _I64, _I, _I]),
+    "mom_linear_ce_fwd": (_I, [_VP, _VP, _VP, _I, _I64, _I, _I64, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "mom_linear_ce_bwd": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I64, _I, _I64, _VP, _VP, _VP, _SZ, _VP]),
 }
 
 
@@ -610,3 +621,171 @@ def mom_decode_step_rule(x, weights: MomWeights, H, d, n_mem, top_k, scale, rule
     _check(lib.mom_decode_step_rule(_p(x), ctypes.byref(weights), mg, B, d_model, H, d, n_mem, top_k, float(scale),
                                     dtype_code(x.dtype), int(rule), _p(state), _p(out), _p(topk_idx), _p(ws),
                                     ws.numel(), _s(stream)), "mom_decode_step_rule")
+
+
+# --------------------------------------- around the blocks in a training step
+
+MOM_ACT8_GROUP, MOM_NORM_MAX_D = 128, 16384
+MOM_GATE_NONE, MOM_GATE_TOKEN, MOM_GATE_ELEMENT = 0, 1, 2
+
+
+def _want(name, t, shape, dtypes, like):
+    """The library reads and writes as many elements as the sizes say: a tensor
+    of another shape, type or device is refused here."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("MoM: %s has shape %s, %s is wanted" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype not in dtypes:
+        raise ValueError("MoM: %s is %s, %s is wanted" % (name, t.dtype, " or ".join(str(d) for d in dtypes)))
+    if t.device != like.device:
+        raise ValueError("MoM: %s is on %s, not on %s" % (name, t.device, like.device))
+
+
+def _run(what, like, stream, fn, *args):
+    """fn(*args, stream) on the device of ``like``."""
+    if like.is_cuda and like.device.index != torch.cuda.current_device():
+        with torch.cuda.device(like.device):
+            _check(fn(*args, _s(stream)), what)
+    else:
+        _check(fn(*args, _s(stream)), what)
+
+
+_F32, _ANY = (torch.float32,), (torch.float32, torch.bfloat16)
+
+
+def new_act8(n_rows, d, device=None):
+    """An 8-bit checkpoint's tensors: (codes int8 [n_rows, d], scales float32
+    [n_rows, ceil(d / 128)])."""
+    dev = device or "cuda"
+    return (torch.empty((n_rows, d), dtype=torch.int8, device=dev),
+            torch.empty((n_rows, -(-d // MOM_ACT8_GROUP)), dtype=torch.float32, device=dev))
+
+
+def _want_act8(k8, n, d, like):
+    codes, scales = k8
+    _want("codes", codes, (n, d), (torch.int8,), like)
+    _want("scales", scales, (n, -(-d // MOM_ACT8_GROUP)), _F32, like)
+    return codes, scales
+
+
+def mom_act_pack8(x, k8, stream=None):
+    """x [n, d] -> the 8-bit checkpoint k8 = (codes, scales) (new_act8)."""
+    n, d = x.shape
+    codes, scales = _want_act8(k8, n, d, x)
+    _run("mom_act_pack8", x, stream, lib.mom_act_pack8, _p(x), dtype_code(x.dtype), n, d, _p(codes), _p(scales))
+
+
+def mom_act_unpack8(k8, x, stream=None):
+    """The restored values of the checkpoint k8 into x [n, d]."""
+    n, d = x.shape
+    codes, scales = _want_act8(k8, n, d, x)
+    _run("mom_act_unpack8", x, stream, lib.mom_act_unpack8, _p(codes), _p(scales), n, d, _p(x), dtype_code(x.dtype))
+
+
+def _res_norm(x, y, gate, w_post, res_scale, w_pre, x_dt, dt):
+    """(x, codes, scales, gate mode, n, d) of the residual norm's calls, its
+    operands' shapes checked."""
+    codes = scales = None
+    if isinstance(x, (tuple, list)):
+        n, d = x[0].shape
+        codes, scales = _want_act8(x, n, d, x[0])
+        like, x = x[0], None
+    else:
+        n, d = x.shape
+        _want("x", x, (n, d), (x_dt,), x)
+        like = x
+    mode = MOM_GATE_NONE
+    _want("y", y, (n, d), (dt,), like)
+    if gate is not None:
+        elem = gate.dim() == 2 and tuple(gate.shape) == (n, d) and d > 1
+        mode = MOM_GATE_ELEMENT if elem else MOM_GATE_TOKEN
+        if not elem and tuple(gate.shape) not in ((n,), (n, 1)):
+            raise ValueError("MoM: gate has shape %s, (%d,), (%d, 1) or (%d, %d) is wanted"
+                             % (tuple(gate.shape), n, n, n, d))
+        _want("gate", gate, gate.shape, (dt,), like)
+    for name, w in (("w_post", w_post), ("res_scale", res_scale), ("w_pre", w_pre)):
+        _want(name, w, (d,), _F32, like)
+    return like, x, codes, scales, mode, n, d
+
+
+def mom_residual_norm(x, y, gate, w_post, res_scale, w_pre, eps, x_out, h, pack=None, stream=None):
+    """x_out = x + res_scale * sigmoid(gate) * rmsnorm(y) * w_post and h =
+    rmsnorm(x_out) * w_pre.  x [n, d], or (codes, scales) of its 8-bit
+    checkpoint; y None: no block (x_out = x); gate None, [n], [n, 1] or [n, d];
+    res_scale None: 1; x_out, h: None where not wanted; pack: (codes, scales)
+    that receive x's 8-bit checkpoint."""
+    q8 = isinstance(x, (tuple, list))
+    x_dt = x_out.dtype if q8 and x_out is not None else torch.float32 if q8 else x.dtype
+    dt = next((t.dtype for t in (y, h, gate) if t is not None), x_dt)
+    like, x, codes, scales, mode, n, d = _res_norm(x, y, gate, w_post, res_scale, w_pre, x_dt, dt)
+    _want("x_out", x_out, (n, d), (x_dt,), like)
+    _want("h", h, (n, d), (dt,), like)
+    p_codes, p_scales = _want_act8(pack, n, d, like) if pack is not None else (None, None)
+    _run("mom_residual_norm", like, stream, lib.mom_residual_norm, _p(x), _p(codes), _p(scales), _p(y), _p(gate), mode,
+         _p(w_post), _p(res_scale), _p(w_pre), float(eps), n, d, dtype_code(x_dt), dtype_code(dt), _p(x_out), _p(h),
+         _p(p_codes), _p(p_scales))
+
+
+def mom_residual_norm_bwd_workspace_size(n_rows, d):
+    return lib.mom_residual_norm_bwd_workspace_size(n_rows, d)
+
+
+def mom_residual_norm_bwd(x, y, gate, w_post, res_scale, w_pre, eps, dx_out, dh, dx, dy, dgate, dw_post, dres_scale,
+                          dw_pre, ws, stream=None):
+    """The adjoint of mom_residual_norm at the same x, y, gate and weights:
+    from dx_out and dh (None: 0 / no pre-norm) the gradients dx, dy, dgate (the
+    gate's shape), dw_post, dres_scale, dw_pre (None where not wanted)."""
+    q8 = isinstance(x, (tuple, list))
+    x_dt = torch.float32 if q8 else x.dtype
+    dt = next((t.dtype for t in (y, dy, gate) if t is not None), x_dt)
+    like, x, codes, scales, mode, n, d = _res_norm(x, y, gate, w_post, res_scale, w_pre, x_dt, dt)
+    g_dt = dx.dtype
+    for name, t in (("dx_out", dx_out), ("dh", dh), ("dx", dx)):
+        _want(name, t, (n, d), (g_dt,), like)
+    _want("dy", dy, (n, d), (dt,), like)
+    if dgate is not None and gate is not None:
+        _want("dgate", dgate, gate.shape, (dt,), like)
+    for name, t in (("dw_post", dw_post), ("dres_scale", dres_scale), ("dw_pre", dw_pre)):
+        _want(name, t, (d,), _F32, like)
+    _run("mom_residual_norm_bwd", like, stream, lib.mom_residual_norm_bwd, _p(x), _p(codes), _p(scales), _p(y),
+         _p(gate), mode, _p(w_post), _p(res_scale), _p(w_pre), float(eps), n, d, dtype_code(x_dt), dtype_code(dt),
+         _p(dx_out), _p(dh), dtype_code(g_dt), _p(dx), _p(dy), _p(dgate), _p(dw_post), _p(dres_scale), _p(dw_pre),
+         _p(ws), ws.numel())
+
+
+def mom_linear_ce_workspace_size(n_rows, d, vocab, dt, backward):
+    return lib.mom_linear_ce_workspace_size(n_rows, d, vocab, dtype_code(dt), int(bool(backward)))
+
+
+def _want_ce(x, w, targets):
+    n, d = x.shape
+    vocab = w.shape[0]
+    _want("x", x, (n, d), _ANY, x)
+    _want("w", w, (vocab, d), (x.dtype,), x)
+    _want("targets", targets, (n,), (torch.int32,), x)
+    return n, d, vocab
+
+
+def mom_linear_ce_fwd(x, w, targets, loss, lse, mean, ws, stream=None):
+    """loss, lse [n] of the logits x w^T (x [n, d], w [vocab, d], targets [n]
+    int32, < 0: padding); mean [2] float32 or None: mean loss, 1 / rows counted."""
+    n, d, vocab = _want_ce(x, w, targets)
+    _want("loss", loss, (n,), _F32, x)
+    _want("lse", lse, (n,), _F32, x)
+    _want("mean", mean, (2,), _F32, x)
+    _run("mom_linear_ce_fwd", x, stream, lib.mom_linear_ce_fwd, _p(x), _p(w), _p(targets), dtype_code(x.dtype), n, d,
+         vocab, _p(loss), _p(lse), _p(mean), _p(ws), ws.numel())
+
+
+def mom_linear_ce_bwd(x, w, targets, lse, dloss, dscale, dx, dw, ws, stream=None):
+    """dx [n, d] and dw [vocab, d] of sum_t dloss[t] dscale loss[t] (dloss [n],
+    dscale [1]; None: 1), lse from the forward."""
+    n, d, vocab = _want_ce(x, w, targets)
+    _want("lse", lse, (n,), _F32, x)
+    _want("dloss", dloss, (n,), _F32, x)
+    _want("dscale", dscale, (1,), _F32, x)
+    _want("dx", dx, (n, d), (x.dtype,), x)
+    _want("dw", dw, (vocab, d), (x.dtype,), x)
+    _run("mom_linear_ce_bwd", x, stream, lib.mom_linear_ce_bwd, _p(x), _p(w), _p(targets), _p(lse), _p(dloss),
+         _p(dscale), dtype_code(x.dtype), n, d, vocab, _p(dx), _p(dw), _p(ws), ws.numel())

@@ -945,4 +945,159 @@ mom_status mom_convert(const void* src, mom_dtype src_dt, void* dst, mom_dtype d
     return cuda_status(launch_convert(src, src_dt, dst, dst_dt, n, as_stream(stream)));
 }
 
+// ------------------------------------------ the residual stream's norms
+namespace {
+inline bool al(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// the checks that the forward and the adjoint share; fills `a`
+mom_status res_norm_args(const void* x, const int8_t* x_codes, const float* x_scales, const void* y, const void* gate,
+                         int gate_mode, const float* w_post, const float* res_scale, const float* w_pre, float eps,
+                         int64_t n_rows, int d, int x_dt, int dt, ResNormArgs& a, int& kind, bool& vec) {
+    if (!dt_ok(x_dt) || !dt_ok(dt) || n_rows < 0 || d < 1 || !(eps >= 0.f)) return MOM_ERR_ARG;
+    if (gate_mode != MOM_GATE_NONE && gate_mode != MOM_GATE_TOKEN && gate_mode != MOM_GATE_ELEMENT) return MOM_ERR_ARG;
+    if (d > MOM_NORM_MAX_D || n_rows > 0x7fffffffLL) return MOM_ERR_UNSUPPORTED;
+    if (x && (x_codes || x_scales)) return MOM_ERR_ARG;
+    if (n_rows > 0) {          // (an array of no rows may be NULL)
+        if (!y && (gate || gate_mode != MOM_GATE_NONE || w_post || res_scale)) return MOM_ERR_ARG;
+        if (!x && (!x_codes || !x_scales)) return MOM_ERR_ARG;
+        if ((gate_mode != MOM_GATE_NONE) != (gate != nullptr)) return MOM_ERR_ARG;
+        if (y && !w_post) return MOM_ERR_ARG;
+    }
+    if (x_dt == MOM_BF16 && dt == MOM_F32 && x) return MOM_ERR_UNSUPPORTED;
+    if (!al(x, esize(x_dt)) || !al(y, esize(dt)) || !al(gate, esize(dt)) || !al(x_scales, 4) || !al(w_post, 4) ||
+        !al(res_scale, 4) || !al(w_pre, 4))
+        return MOM_ERR_ARG;
+    a = ResNormArgs{};
+    a.x = x; a.x_codes = x_codes; a.x_scales = x_scales;
+    a.y = y; a.gate = gate; a.gate_mode = gate_mode;
+    a.w_post = w_post; a.res_scale = res_scale; a.w_pre = w_pre;
+    a.eps = eps;
+    a.n_rows = n_rows;
+    a.d = d;
+    a.groups = (int)cdiv(d, MOM_ACT8_GROUP);
+    a.x_out_f32 = x_dt == MOM_F32;
+    kind = !x ? RN_X_Q8 : x_dt == MOM_BF16 ? RN_X_BF16 : RN_X_F32;
+    vec = d % 8 == 0 && al16(x) && al(x_codes, 8) && al16(y) && (gate_mode != MOM_GATE_ELEMENT || al16(gate)) &&
+          al16(w_post) && al16(res_scale) && al16(w_pre);
+    return MOM_OK;
+}
+}  // namespace
+
+mom_status mom_act_pack8(const void* x, mom_dtype dt, int64_t n_rows, int d, int8_t* codes, float* scales,
+                         void* stream) {
+    if (!dt_ok(dt) || n_rows < 0 || d < 1) return MOM_ERR_ARG;
+    if (n_rows == 0) return MOM_OK;
+    if (!x || !codes || !scales || !al(x, esize(dt)) || !al(scales, 4)) return MOM_ERR_ARG;
+    const bool vec = d % 8 == 0 && al16(x) && al(codes, 8);
+    return cuda_status(launch_act8_pack(x, dt, n_rows, d, codes, scales, vec, as_stream(stream)));
+}
+
+mom_status mom_act_unpack8(const int8_t* codes, const float* scales, int64_t n_rows, int d, void* x, mom_dtype dt,
+                           void* stream) {
+    if (!dt_ok(dt) || n_rows < 0 || d < 1) return MOM_ERR_ARG;
+    if (n_rows == 0) return MOM_OK;
+    if (!x || !codes || !scales || !al(x, esize(dt)) || !al(scales, 4)) return MOM_ERR_ARG;
+    const bool vec = d % 8 == 0 && al16(x) && al(codes, 8);
+    return cuda_status(launch_act8_unpack(codes, scales, n_rows, d, x, dt, vec, as_stream(stream)));
+}
+
+mom_status mom_residual_norm(const void* x, const int8_t* x_codes, const float* x_scales, const void* y,
+                             const void* gate, mom_gate_mode gate_mode, const float* w_post, const float* res_scale,
+                             const float* w_pre, float eps, int64_t n_rows, int d, mom_dtype x_dt, mom_dtype dt,
+                             void* x_out, void* h, int8_t* codes_out, float* scales_out, void* stream) {
+    ResNormArgs a;
+    int kind;
+    bool vec;
+    const mom_status s = res_norm_args(x, x_codes, x_scales, y, gate, gate_mode, w_post, res_scale,
+                                       h ? w_pre : nullptr, eps, n_rows, d, x_dt, dt, a, kind, vec);
+    if (s != MOM_OK) return s;
+    if ((codes_out != nullptr) != (scales_out != nullptr) || (codes_out && !x && n_rows > 0)) return MOM_ERR_ARG;
+    if (!al(x_out, esize(x_dt)) || !al(h, esize(dt)) || !al(scales_out, 4)) return MOM_ERR_ARG;
+    if (n_rows == 0) return MOM_OK;
+    if (!x_out && !h && !codes_out) return MOM_ERR_ARG;
+    if (h && !w_pre) return MOM_ERR_ARG;
+    a.x_out = x_out; a.h = h;
+    a.codes_out = codes_out; a.scales_out = scales_out;
+    vec = vec && al16(x_out) && al16(h) && al(codes_out, 8);
+    return cuda_status(launch_residual_norm(a, kind, dt, vec, as_stream(stream)));
+}
+
+size_t mom_residual_norm_bwd_workspace_size(int64_t n_rows, int d) {
+    if (n_rows < 0 || d < 1 || d > MOM_NORM_MAX_D) return MOM_WS_HEADER_BYTES;
+    return MOM_WS_HEADER_BYTES + up256((size_t)residual_norm_bwd_parts(n_rows, d) * 2 * d * 4);
+}
+
+mom_status mom_residual_norm_bwd(const void* x, const int8_t* x_codes, const float* x_scales, const void* y,
+                                 const void* gate, mom_gate_mode gate_mode, const float* w_post,
+                                 const float* res_scale, const float* w_pre, float eps, int64_t n_rows, int d,
+                                 mom_dtype x_dt, mom_dtype dt, const void* dx_out, const void* dh, mom_dtype g_dt,
+                                 void* dx, void* dy, void* dgate, float* dw_post, float* dres_scale, float* dw_pre,
+                                 void* ws, size_t ws_bytes, void* stream) {
+    ResNormArgs a;
+    int kind;
+    bool vec;
+    if (!dt_ok(g_dt)) return MOM_ERR_ARG;
+    const mom_status s = res_norm_args(x, x_codes, x_scales, y, gate, gate_mode, w_post, res_scale,
+                                       dh ? w_pre : nullptr, eps, n_rows, d, x_dt, dt, a, kind, vec);
+    if (s != MOM_OK) return s;
+    if (!al(dx_out, esize(g_dt)) || !al(dh, esize(g_dt)) || !al(dx, esize(g_dt)) || !al(dy, esize(dt)) ||
+        !al(dgate, esize(dt)) || !al(dw_post, 4) || !al(dres_scale, 4) || !al(dw_pre, 4))
+        return MOM_ERR_ARG;
+    if (!ws || !al16(ws) || ws_bytes < mom_residual_norm_bwd_workspace_size(n_rows, d)) return MOM_ERR_ARG;
+    if ((dres_scale && !res_scale) || (dres_scale && !w_post)) return MOM_ERR_ARG;
+    if (n_rows > 0) {
+        if (!y && (dy || dgate || dw_post || dres_scale)) return MOM_ERR_ARG;
+        if (dgate && gate_mode == MOM_GATE_NONE) return MOM_ERR_ARG;
+        if (!dx || (!dx_out && !dh) || (y && !dy) || (dh && !w_pre) || (dw_pre && !dh)) return MOM_ERR_ARG;
+    }
+    ResNormBwdArgs b{dx_out, dh, dx, dy, dgate, dw_post, dres_scale, dw_pre,
+                     reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + MOM_WS_HEADER_BYTES)};
+    vec = vec && al16(dx_out) && al16(dh) && al16(dx) && al16(dy) &&
+          (gate_mode != MOM_GATE_ELEMENT || al16(dgate));
+    return cuda_status(launch_residual_norm_bwd(a, b, kind, dt, g_dt, vec, as_stream(stream)));
+}
+
+// ------------------------------------------------- vocabulary cross entropy
+size_t mom_linear_ce_workspace_size(int64_t n_rows, int d, int64_t vocab, mom_dtype dt, int backward) {
+    if (!dt_ok(dt) || n_rows < 0 || d < 1 || vocab < 1) return MOM_WS_HEADER_BYTES;
+    return linear_ce_workspace_bytes(n_rows, d, vocab, dt, backward != 0);
+}
+
+static mom_status linear_ce_ok(const void* x, const void* w, const int32_t* targets, int dt, int64_t n_rows, int d,
+                               int64_t vocab, const void* ws, size_t ws_bytes, bool bwd) {
+    if (!dt_ok(dt) || n_rows < 0 || d < 1 || vocab < 1) return MOM_ERR_ARG;
+    if (n_rows > (1LL << 30) || vocab > (1LL << 30) || d > (1 << 20)) return MOM_ERR_UNSUPPORTED;
+    if (!ws || !al16(ws) || ws_bytes < mom_linear_ce_workspace_size(n_rows, d, vocab, dt, bwd)) return MOM_ERR_ARG;
+    if (n_rows > 0 && (!x || !w || !targets || !al16(x) || !al16(w) || !al(targets, 4))) return MOM_ERR_ARG;
+    return MOM_OK;
+}
+
+mom_status mom_linear_ce_fwd(const void* x, const void* w, const int32_t* targets, mom_dtype dt, int64_t n_rows,
+                             int d, int64_t vocab, float* loss, float* lse, float* mean, void* ws, size_t ws_bytes,
+                             void* stream) {
+    const mom_status s = linear_ce_ok(x, w, targets, dt, n_rows, d, vocab, ws, ws_bytes, false);
+    if (s != MOM_OK) return s;
+    if ((n_rows > 0 && (!loss || !lse)) || !al(loss, 4) || !al(lse, 4) || !al(mean, 4)) return MOM_ERR_ARG;
+    if (n_rows == 0) return mean ? cuda_status(cudaMemsetAsync(mean, 0, 8, as_stream(stream))) : MOM_OK;
+    if (!device_is_sm100() || !tma_available()) return MOM_ERR_UNSUPPORTED;
+    LinearCeArgs a{};
+    a.x = x; a.w = w; a.targets = targets; a.dt = dt; a.n = n_rows; a.v = vocab; a.d = d;
+    a.loss = loss; a.lse = lse; a.mean = mean; a.ws = ws;
+    return cuda_status(launch_linear_ce_fwd(a, as_stream(stream)));
+}
+
+mom_status mom_linear_ce_bwd(const void* x, const void* w, const int32_t* targets, const float* lse,
+                             const float* dloss, const float* dscale, mom_dtype dt, int64_t n_rows, int d,
+                             int64_t vocab, void* dx, void* dw, void* ws, size_t ws_bytes, void* stream) {
+    const mom_status s = linear_ce_ok(x, w, targets, dt, n_rows, d, vocab, ws, ws_bytes, true);
+    if (s != MOM_OK) return s;
+    if (!dw || !al16(dw) || !al16(dx) || !al(lse, 4) || !al(dloss, 4) || !al(dscale, 4)) return MOM_ERR_ARG;
+    if (n_rows == 0) return cuda_status(cudaMemsetAsync(dw, 0, (size_t)vocab * d * esize(dt), as_stream(stream)));
+    if (!lse || !dx) return MOM_ERR_ARG;
+    if (!device_is_sm100() || !tma_available()) return MOM_ERR_UNSUPPORTED;
+    LinearCeArgs a{};
+    a.x = x; a.w = w; a.targets = targets; a.dt = dt; a.n = n_rows; a.v = vocab; a.d = d;
+    a.lse = const_cast<float*>(lse); a.dloss = dloss; a.dscale = dscale; a.dx = dx; a.dw = dw; a.ws = ws;
+    return cuda_status(launch_linear_ce_bwd(a, as_stream(stream)));
+}
+
 }  // extern "C"

@@ -29,6 +29,11 @@ bool make_tma_2d_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t 
 // Same without swizzle (row-major shared tile, e.g. an output staging tile).
 bool make_tma_2d_bf16_plain(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t row_pitch_elems,
                             uint32_t box_cols, uint32_t box_rows);
+// [parts][rows][row_pitch] matrices of bf16 or float32, the inner extent `inner`;
+// boxes of box_rows x 128 bytes of one part (128-byte swizzle).  The parts lie
+// part_rows rows apart (0: rows).  row_pitch a multiple of 16 bytes.
+bool make_tma_3d(CUtensorMap* m, const void* base, bool f32, uint64_t inner, uint64_t rows, uint64_t parts,
+                 uint64_t row_pitch_elems, uint32_t box_rows, uint64_t part_rows = 0);
 bool device_is_sm100();
 
 // router.cu
@@ -274,5 +279,59 @@ struct ConvBwdArgs {
 };
 cudaError_t launch_conv_bwd(const ConvBwdArgs* problems, int n, int C, int W, int d, void* err, cudaStream_t st);
 cudaError_t launch_convert(const void* src, int src_dt, void* dst, int dst_dt, int64_t n, cudaStream_t st);
+
+// act8.cu: 8-bit activation checkpoints.  `vec`: d % 8 == 0 and every array
+// aligned for 16-byte (codes: 8-byte) accesses.
+cudaError_t launch_act8_pack(const void* x, int dt, int64_t n_rows, int d, int8_t* codes, float* scales, bool vec,
+                             cudaStream_t st);
+cudaError_t launch_act8_unpack(const int8_t* codes, const float* scales, int64_t n_rows, int d, void* x, int dt,
+                               bool vec, cudaStream_t st);
+
+// residual_norm.cu: the residual stream's norms and their adjoint
+enum { RN_X_BF16 = 0, RN_X_F32 = 1, RN_X_Q8 = 2 };
+struct ResNormArgs {
+    const void* x;                 // the stream (or x_codes / x_scales)
+    const int8_t* x_codes;
+    const float* x_scales;
+    const void *y, *gate;          // block type; null: no block / no gate
+    int gate_mode;
+    const float *w_post, *res_scale, *w_pre;
+    float eps;
+    int64_t n_rows;
+    int d, groups;                 // groups of kActGroup channels a row
+    void *x_out, *h;
+    int x_out_f32;
+    int8_t* codes_out;
+    float* scales_out;
+    int warps_per_row;             // set by the launcher
+};
+struct ResNormBwdArgs {
+    const void *dx_out, *dh;       // gradient type
+    void *dx;                      // gradient type
+    void *dy, *dgate;              // block type
+    float *dw_post, *dres_scale, *dw_pre;
+    float* partial;                // [residual_norm_bwd_parts][2][d]
+};
+int residual_norm_bwd_parts(int64_t n_rows, int d);
+cudaError_t launch_residual_norm(const ResNormArgs& a, int x_kind, int dt, bool vec, cudaStream_t st);
+cudaError_t launch_residual_norm_bwd(const ResNormArgs& a, const ResNormBwdArgs& b, int x_kind, int dt, int g_dt,
+                                     bool vec, cudaStream_t st);
+
+// linear_ce.cu: softmax cross entropy of x W^T without the logits
+struct LinearCeArgs {
+    const void *x, *w;             // [n, d], [v, d]
+    const int32_t* targets;        // [n]
+    int dt;
+    int64_t n, v;
+    int d;
+    float *loss, *lse;             // [n]
+    float* mean;                   // [2] or null: mean loss, 1 / rows counted
+    const float *dloss, *dscale;   // backward: [n] or null, [1] or null
+    void *dx, *dw;
+    void* ws;
+};
+size_t linear_ce_workspace_bytes(int64_t n, int d, int64_t v, int dt, bool bwd);
+cudaError_t launch_linear_ce_fwd(const LinearCeArgs& a, cudaStream_t st);
+cudaError_t launch_linear_ce_bwd(const LinearCeArgs& a, cudaStream_t st);
 
 }  // namespace mom

@@ -50,6 +50,20 @@ bool make_tma_2d_bf16_plain(CUtensorMap* m, const void* base, uint64_t rows, uin
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tma_3d(CUtensorMap* m, const void* base, bool f32, uint64_t inner, uint64_t rows, uint64_t parts,
+                 uint64_t row_pitch_elems, uint32_t box_rows, uint64_t part_rows) {
+    auto fn = encode_fn();
+    if (!fn || rows == 0 || inner == 0 || parts == 0) return false;
+    const uint64_t es = f32 ? 4 : 2;
+    cuuint64_t dims[3] = {inner, rows, parts};
+    cuuint64_t strides[2] = {row_pitch_elems * es, row_pitch_elems * es * (part_rows ? part_rows : rows)};
+    cuuint32_t box[3] = {f32 ? 32u : 64u, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool device_is_sm100() {
     int dev = 0, major = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;

@@ -1,0 +1,143 @@
+"""A stack of Mixture-of-Memories blocks in a residual stream, on the GPU.
+
+    h_0     = norm(x_0) w_pre[0]
+    y_i     = block_i(h_i)
+    x_{i+1} = x_i + res_scale[i] sigmoid(gate_i) norm(y_i) w_post[i]
+    h_{i+1} = norm(x_{i+1}) w_pre[i+1]          (the last one: w_final)
+
+The norms, gates and additions between two blocks are one call
+(mom_residual_norm), which also keeps the block's input stream as an 8-bit
+checkpoint: the backward pass restores the blocks' inputs and the stream from
+it (mom_residual_norm, mom_residual_norm_bwd) instead of from x_i and h_i.
+Everything runs in the CUDA library; this module holds buffers and passes
+pointers.
+"""
+from __future__ import annotations
+
+from typing import Dict, List, Optional, Sequence
+
+import torch
+
+from . import binding as B
+from .block import MoMBlock, RMS_EPS
+
+
+class MoMStack:
+    """blocks: MoMBlock, one a level; norms: for each level a dict of w_pre,
+    w_post [d_model] and optionally res_scale [d_model], float32; w_final
+    [d_model]: the norm after the last block.  ``stream_dtype``: the residual
+    stream's type (bf16 or float32)."""
+
+    def __init__(self, blocks: Sequence[MoMBlock], norms: Sequence[Dict[str, torch.Tensor]], w_final: torch.Tensor,
+                 eps: float = RMS_EPS, stream_dtype: torch.dtype = torch.bfloat16):
+        if len(blocks) != len(norms) or not blocks:
+            raise ValueError("one norms entry a block")
+        if len(set(id(b) for b in blocks)) != len(blocks):
+            raise ValueError("every level has a block of its own (it keeps its forward's activations)")
+        B.dtype_code(stream_dtype)
+        self.blocks, self.norms, self.w_final, self.eps = list(blocks), list(norms), w_final, eps
+        self.dtype, self.stream_dtype = blocks[0].dtype, stream_dtype
+        self.d_model, self.device = blocks[0].d_model, blocks[0].device
+        if any(b.d_model != self.d_model for b in blocks):
+            raise ValueError("the blocks' d_model differ")
+        self._bufs = {}
+
+    def _buf(self, name, shape, dtype):
+        key = (name, tuple(shape), dtype)
+        t = self._bufs.get(key)
+        if t is None:
+            t = self._bufs[key] = torch.empty(shape, dtype=dtype, device=self.device)
+        return t
+
+    def _k8(self, i, n):
+        groups = -(-self.d_model // B.MOM_ACT8_GROUP)
+        return (self._buf("codes%d" % i, (n, self.d_model), torch.int8),
+                self._buf("scales%d" % i, (n, groups), torch.float32))
+
+    def _w_next(self, i):
+        return self.norms[i + 1]["w_pre"] if i + 1 < len(self.blocks) else self.w_final
+
+    # -------------------------------------------------------------- forward
+    def forward(self, x: torch.Tensor, cu_seqlens: torch.Tensor, gates: Optional[List] = None,
+                stream=None) -> Dict[str, torch.Tensor]:
+        """x [N, d_model] (stream_dtype), cu_seqlens [S+1] int32 (device);
+        gates: None, or one entry a block (None, or logits [N], [N, 1] or
+        [N, d_model] in the blocks' type).  Returns ``h`` [N, d_model], the
+        normed output, and ``x``, the stream after the last block (both
+        written again by the next call); x itself is left as it is."""
+        n = x.shape[0]
+        st = stream if stream is not None else torch.cuda.current_stream()
+        h = self._buf("h", (n, self.d_model), self.dtype)
+        out = self._buf("x", (n, self.d_model), self.stream_dtype)
+        B.mom_residual_norm(x, None, None, None, None, self.norms[0]["w_pre"], self.eps, None, h, stream=st)
+        for i, blk in enumerate(self.blocks):
+            y = blk.forward(h, cu_seqlens, stream=st)["y"]
+            w = self.norms[i]
+            B.mom_residual_norm(x, y, gates[i] if gates else None, w["w_post"], w.get("res_scale"), self._w_next(i),
+                                self.eps, out, h, pack=self._k8(i, n), stream=st)
+            x = out
+        return dict(h=h, x=out)
+
+    # ------------------------------------------------------------- backward
+    def backward(self, cu_seqlens: torch.Tensor, dh: torch.Tensor, dx: Optional[torch.Tensor] = None,
+                 gates: Optional[List] = None, stream=None) -> Dict:
+        """Gradients of <dh, h> + <dx, x> for the forward just run with the
+        same cu_seqlens and gates (its checkpoints and the blocks' buffers are
+        read; dh, dx [N, d_model] float32).  Returns ``dx`` [N, d_model]
+        float32, the gradient of the input stream, ``dw_final`` and ``levels``:
+        for each block dw_pre, dw_post, dres_scale, dgate (where it has them)
+        and ``block``, the block's own gradients (MoMBlock.backward)."""
+        n = dh.shape[0]
+        st = stream if stream is not None else torch.cuda.current_stream()
+        f32 = torch.float32
+        g = self._buf("dx", (n, self.d_model), f32)
+        ws = self._bufs.get(("ws", n))
+        if ws is None:
+            with torch.cuda.stream(st):
+                ws = self._bufs[("ws", n)] = B.new_workspace(B.mom_residual_norm_bwd_workspace_size(n, self.d_model),
+                                                             self.device)
+        levels: List[Dict] = [None] * len(self.blocks)
+        vec = lambda name, i: self._buf("%s%d" % (name, i), (self.d_model,), f32)
+        dw_next = vec("dw_final", 0)
+        dw_final = dw_next
+        h = self._buf("h_restored", (n, self.d_model), self.dtype)      # (the forward's h stays the caller's)
+        dy = self._buf("dy", (n, self.d_model), self.dtype)
+        for i in reversed(range(len(self.blocks))):
+            blk, w, k8 = self.blocks[i], self.norms[i], self._k8(i, n)
+            gate = gates[i] if gates else None
+            lev = dict(dw_post=vec("dw_post", i))
+            if w.get("res_scale") is not None:
+                lev["dres_scale"] = vec("dres_scale", i)
+            if gate is not None:
+                lev["dgate"] = self._buf("dgate%d" % i, gate.shape, gate.dtype)
+            y = blk.block_buffers(n, cu_seqlens.numel() - 1)["y"]
+            B.mom_residual_norm_bwd(k8, y, gate, w["w_post"], w.get("res_scale"), self._w_next(i), self.eps, dx, dh, g,
+                                    dy, lev.get("dgate"), lev["dw_post"], lev.get("dres_scale"), dw_next, ws, stream=st)
+            B.mom_residual_norm(k8, None, None, None, None, w["w_pre"], self.eps, None, h, stream=st)
+            lev["block"] = blk.backward(h, cu_seqlens, dy, stream=st)
+            levels[i] = lev
+            dx, dh, dw_next = g, lev["block"]["dx"], vec("dw_pre", i)
+            lev["dw_pre"] = dw_next
+        # the norm before the first block
+        B.mom_residual_norm_bwd(self._k8(0, n), None, None, None, None, self.norms[0]["w_pre"], self.eps, dx, dh, g, None,
+                                None, None, None, dw_next, ws, stream=st)
+        return dict(dx=g, dw_final=dw_final, levels=levels)
+
+    # --------------------------------------------------------------- decode
+    def decode_step(self, x: torch.Tensor, states: Sequence, gates: Optional[List] = None,
+                    stream=None) -> Dict[str, torch.Tensor]:
+        """One token a sequence: x [B, d_model] (stream_dtype); states: for
+        each block (state, conv_sh, conv_mem) of MoMBlock.decode_step, updated
+        in place.  Returns ``h`` and ``x`` as forward."""
+        n = x.shape[0]
+        st = stream if stream is not None else torch.cuda.current_stream()
+        h = self._buf("dec_h", (n, self.d_model), self.dtype)
+        out = self._buf("dec_x", (n, self.d_model), self.stream_dtype)
+        B.mom_residual_norm(x, None, None, None, None, self.norms[0]["w_pre"], self.eps, None, h, stream=st)
+        for i, blk in enumerate(self.blocks):
+            y, _ = blk.decode_step(h, *states[i], stream=st)
+            w = self.norms[i]
+            B.mom_residual_norm(x, y, gates[i] if gates else None, w["w_post"], w.get("res_scale"), self._w_next(i),
+                                self.eps, out, h, stream=st)
+            x = out
+        return dict(h=h, x=out)

@@ -23,15 +23,25 @@
 namespace mom {
 namespace {
 
-struct Q8 {};      // tag: the stream comes from an 8-bit checkpoint
+template <typename XT, bool VEC> struct RawX {
+    Raw8<XT, VEC> r;
+    __device__ __forceinline__ void load(const ResNormArgs& a, int64_t row, int c0, int lane) {
+        r.load(reinterpret_cast<const XT*>(a.x) + row * a.d, c0, a.d, lane);
+    }
+    __device__ __forceinline__ void get(float* out) const { r.get(out); }
+};
+template <bool VEC> struct RawX<Q8, VEC> {
+    Raw8Q<VEC> r;
+    __device__ __forceinline__ void load(const ResNormArgs& a, int64_t row, int c0, int lane) {
+        r.load(a.x_codes + row * a.d, a.x_scales + row * a.groups, c0, a.d, lane);
+    }
+    __device__ __forceinline__ void get(float* out) const { r.get(out); }
+};
 
-template <typename XT, bool VEC>
-__device__ __forceinline__ void load_x(const ResNormArgs& a, int64_t row, int c0, int lane, float* out) {
-    if constexpr (std::is_same<XT, Q8>::value)
-        act8_load<VEC>(a.x_codes + row * a.d, a.x_scales + row * a.groups, c0, a.d, lane, out);
-    else
-        load8<VEC>(reinterpret_cast<const XT*>(a.x) + row * a.d, c0, a.d, lane, out);
-}
+// sigma(z): the hardware exponential and reciprocal, below 2^-21 relative for
+// |z| < 8 (2^-18 at |z| = 60, where sigma or 1 - sigma is 1e-26); a correctly
+// rounded division cost 15 of the 50 instructions an element took.
+__device__ __forceinline__ float fast_sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
 // Sums of K values over the W = blockDim / 32 warps of a row (every thread
 // gets them); one warp a row needs no barrier.  `buf` alternates so that one
@@ -54,8 +64,8 @@ template <int K> __device__ __forceinline__ void row_sum(float (&v)[K], float* b
 constexpr int kMaxWarps = 16;
 
 // W > 1: a CTA of W warps holds one row.  W == 1: each warp holds its own.
-template <typename XT, typename T, bool VEC, int C>
-__global__ void __launch_bounds__(32 * kMaxWarps) residual_norm_kernel(const ResNormArgs a) {
+template <typename XT, typename T, bool VEC, int C, int MAXW>
+__global__ void __launch_bounds__(32 * MAXW) residual_norm_kernel(const ResNormArgs a) {
     __shared__ float red[2][kMaxWarps];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const int W = a.warps_per_row, warp = W > 1 ? wid : 0;
@@ -63,51 +73,67 @@ __global__ void __launch_bounds__(32 * kMaxWarps) residual_norm_kernel(const Res
     if (row >= a.n_rows) return;      // whole CTAs (W > 1) or whole warps (W == 1)
     const int d = a.d;
     const float inv_d = 1.f / (float)d;
-    float xv[C][8], yv[C][8], gv[C][8];
-#pragma unroll
-    for (int j = 0; j < C; ++j) load_x<XT, VEC>(a, row, (warp + j * W) * kChunk, lane, xv[j]);
+    RawX<XT, VEC> xr[C];
+    float xv[C][8];
     if (a.y) {
-        const T* y = reinterpret_cast<const T*>(a.y) + row * d;
-#pragma unroll
-        for (int j = 0; j < C; ++j) load8<VEC>(y, (warp + j * W) * kChunk, d, lane, yv[j]);
-        if (a.gate_mode == MOM_GATE_ELEMENT) {
-            const T* g = reinterpret_cast<const T*>(a.gate) + row * d;
-#pragma unroll
-            for (int j = 0; j < C; ++j) load8<VEC>(g, (warp + j * W) * kChunk, d, lane, gv[j]);
-        }
-        const float gt = a.gate_mode == MOM_GATE_TOKEN ? sigmoidf_(to_f(reinterpret_cast<const T*>(a.gate)[row])) : 1.f;
-        if (a.codes_out) {
-#pragma unroll
-            for (int j = 0; j < C; ++j)
-                act8_store<VEC>(xv[j], (warp + j * W) * kChunk, d, lane, a.codes_out + row * d,
-                                a.scales_out + row * a.groups);
-        }
-        float ss[1] = {0.f};
+        Raw8<T, VEC> yr[C], gr[C];
 #pragma unroll
         for (int j = 0; j < C; ++j)
+            yr[j].load(reinterpret_cast<const T*>(a.y) + row * d, (warp + j * W) * kChunk, d, lane);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss[0] = fmaf(yv[j][i], yv[j][i], ss[0]);
+        for (int j = 0; j < C; ++j) xr[j].load(a, row, (warp + j * W) * kChunk, lane);
+        if (a.gate_mode == MOM_GATE_ELEMENT) {
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                gr[j].load(reinterpret_cast<const T*>(a.gate) + row * d, (warp + j * W) * kChunk, d, lane);
+        }
+        float gt = 1.f;
+        if (a.gate_mode == MOM_GATE_TOKEN) gt = fast_sigmoid(to_f(reinterpret_cast<const T*>(a.gate)[row]));
+        float ss[1] = {0.f};
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            float y[8];
+            yr[j].get(y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss[0] = fmaf(y[i], y[i], ss[0]);
+        }
         row_sum<1>(ss, red[0], W, warp, lane);
-        const float ry = 1.f / sqrtf(ss[0] * inv_d + a.eps);
+        const float ry = gt / sqrtf(ss[0] * inv_d + a.eps);      // 1 / rms(y), times a token's gate
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             const int c0 = (warp + j * W) * kChunk;
-            float w[8], s[8];
+            float y[8], w[8];
+            yr[j].get(y);
+            xr[j].get(xv[j]);
+            if (a.codes_out)
+                act8_store<VEC>(xv[j], c0, d, lane, a.codes_out + row * d, a.scales_out + row * a.groups);
             load8<VEC>(a.w_post, c0, d, lane, w);
-            if (a.res_scale) load8<VEC>(a.res_scale, c0, d, lane, s);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float u = yv[j][i] * ry * w[i];
-                u *= a.gate_mode == MOM_GATE_ELEMENT ? sigmoidf_(gv[j][i]) : gt;
-                if (a.res_scale) u *= s[i];
-                xv[j][i] += u;
+            for (int i = 0; i < 8; ++i) w[i] *= y[i] * ry;
+            if (a.gate_mode == MOM_GATE_ELEMENT) {
+                gr[j].get(y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] *= fast_sigmoid(y[i]);
+            }
+            if (a.res_scale) {
+                load8<VEC>(a.res_scale, c0, d, lane, y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) xv[j][i] = fmaf(w[i], y[i], xv[j][i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) xv[j][i] += w[i];
             }
         }
-    } else if (a.codes_out) {
+    } else {
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-            act8_store<VEC>(xv[j], (warp + j * W) * kChunk, d, lane, a.codes_out + row * d,
-                            a.scales_out + row * a.groups);
+        for (int j = 0; j < C; ++j) xr[j].load(a, row, (warp + j * W) * kChunk, lane);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            xr[j].get(xv[j]);
+            if (a.codes_out)
+                act8_store<VEC>(xv[j], (warp + j * W) * kChunk, d, lane, a.codes_out + row * d,
+                                a.scales_out + row * a.groups);
+        }
     }
     if (a.x_out) {
 #pragma unroll
@@ -137,12 +163,37 @@ __global__ void __launch_bounds__(32 * kMaxWarps) residual_norm_kernel(const Res
     }
 }
 
-// The adjoint.  A CTA walks rows blockIdx.x, + gridDim.x, ..; its threads keep
-// the two column sums (A and dw_pre) of their channels in registers and write
-// them once as the CTA's partial, which cols_reduce_kernel adds up in CTA
-// order: no atomics, the same sums every time on the same device.
-template <typename XT, typename T, typename G, bool VEC, int C>
-__global__ void __launch_bounds__(32 * kMaxWarps) residual_norm_bwd_kernel(const ResNormArgs a, const ResNormBwdArgs b) {
+// A row's operands of the adjoint, as they lie in memory.
+template <typename XT, typename T, typename G, bool VEC, int C> struct BwdRow {
+    RawX<XT, VEC> x[C];
+    Raw8<T, VEC> y[C], g[C];
+    Raw8<G, VEC> d[C], h[C];
+    T gate;
+    __device__ __forceinline__ void load(const ResNormArgs& a, const ResNormBwdArgs& b, int64_t row, int warp, int W,
+                                         int lane) {
+        if (row >= a.n_rows) return;
+        const int n = a.d;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const int c0 = (warp + j * W) * kChunk;
+            if (a.y) y[j].load(reinterpret_cast<const T*>(a.y) + row * n, c0, n, lane);
+            x[j].load(a, row, c0, lane);
+            if (a.gate_mode == MOM_GATE_ELEMENT) g[j].load(reinterpret_cast<const T*>(a.gate) + row * n, c0, n, lane);
+            if (b.dh) h[j].load(reinterpret_cast<const G*>(b.dh) + row * n, c0, n, lane);
+            if (b.dx_out) d[j].load(reinterpret_cast<const G*>(b.dx_out) + row * n, c0, n, lane);
+        }
+        if (a.gate_mode == MOM_GATE_TOKEN) gate = reinterpret_cast<const T*>(a.gate)[row];
+    }
+};
+
+// The adjoint.  A CTA walks rows blockIdx.x, + gridDim.x, ..; the next row's
+// operands are loaded (packed) before this row's arithmetic, so that loads are
+// in flight through its three reductions.  Its threads keep the two column
+// sums (A and dw_pre) of their channels in registers and write them once as
+// the CTA's partial, which cols_reduce_kernel adds up in CTA order: no
+// atomics, the same sums every time on the same device.
+template <typename XT, typename T, typename G, bool VEC, int C, int MAXW>
+__global__ void __launch_bounds__(32 * MAXW) residual_norm_bwd_kernel(const ResNormArgs a, const ResNormBwdArgs b) {
     __shared__ float red[3][2 * kMaxWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     const int d = a.d;
@@ -152,76 +203,83 @@ __global__ void __launch_bounds__(32 * kMaxWarps) residual_norm_bwd_kernel(const
     for (int j = 0; j < C; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) accA[j][i] = accP[j][i] = 0.f;
+    BwdRow<XT, T, G, VEC, C> next;
+    next.load(a, b, blockIdx.x, warp, W, lane);
     for (int64_t row = blockIdx.x; row < a.n_rows; row += gridDim.x) {
+        const BwdRow<XT, T, G, VEC, C> r = next;
+        next.load(a, b, row + gridDim.x, warp, W, lane);
         float xv[C][8], yv[C][8], gv[C][8], dv[C][8], hv[C][8];
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            const int c0 = (warp + j * W) * kChunk;
-            load_x<XT, VEC>(a, row, c0, lane, xv[j]);
-            if (a.y) load8<VEC>(reinterpret_cast<const T*>(a.y) + row * d, c0, d, lane, yv[j]);
-            if (a.gate_mode == MOM_GATE_ELEMENT)
-                load8<VEC>(reinterpret_cast<const T*>(a.gate) + row * d, c0, d, lane, gv[j]);
-            if (b.dx_out) {
-                load8<VEC>(reinterpret_cast<const G*>(b.dx_out) + row * d, c0, d, lane, dv[j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dv[j][i] = 0.f;
-            }
-            if (b.dh) load8<VEC>(reinterpret_cast<const G*>(b.dh) + row * d, c0, d, lane, hv[j]);
-        }
-        const float gt = a.gate_mode == MOM_GATE_TOKEN ? sigmoidf_(to_f(reinterpret_cast<const T*>(a.gate)[row])) : 1.f;
+        float gt = 1.f;
+        if (a.gate_mode == MOM_GATE_TOKEN) gt = fast_sigmoid(to_f(r.gate));
         float ry = 0.f;
         if (a.y) {
             float ss[1] = {0.f};
 #pragma unroll
-            for (int j = 0; j < C; ++j)
+            for (int j = 0; j < C; ++j) {
+                r.y[j].get(yv[j]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) ss[0] = fmaf(yv[j][i], yv[j][i], ss[0]);
+            }
             row_sum<1>(ss, red[0], W, warp, lane);
             ry = 1.f / sqrtf(ss[0] * inv_d + a.eps);
 #pragma unroll
-            for (int j = 0; j < C; ++j)
+            for (int j = 0; j < C; ++j) {
+                if (a.gate_mode == MOM_GATE_ELEMENT) r.g[j].get(gv[j]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     yv[j][i] *= ry;                                       // n_y
-                    gv[j][i] = a.gate_mode == MOM_GATE_ELEMENT ? sigmoidf_(gv[j][i]) : gt;
+                    gv[j][i] = a.gate_mode == MOM_GATE_ELEMENT ? fast_sigmoid(gv[j][i]) : gt;
                 }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            if (b.dx_out) {
+                r.d[j].get(dv[j]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dv[j][i] = 0.f;
+            }
         }
         if (b.dh) {
             float ss[2] = {0.f, 0.f};
-            float dn[C][8];
 #pragma unroll
             for (int j = 0; j < C; ++j) {
                 const int c0 = (warp + j * W) * kChunk;
                 float w[8];
+                r.x[j].get(xv[j]);
+                r.h[j].get(hv[j]);
                 if (a.y) {
-                    float s[8];
                     load8<VEC>(a.w_post, c0, d, lane, w);
-                    if (a.res_scale) load8<VEC>(a.res_scale, c0, d, lane, s);
+                    if (a.res_scale) {
+                        float s[8];
+                        load8<VEC>(a.res_scale, c0, d, lane, s);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float coef = a.res_scale ? w[i] * s[i] : w[i];
-                        xv[j][i] = fmaf(yv[j][i] * gv[j][i], coef, xv[j][i]);   // x'
+                        for (int i = 0; i < 8; ++i) w[i] *= s[i];
                     }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) xv[j][i] = fmaf(yv[j][i] * gv[j][i], w[i], xv[j][i]);   // x'
                 }
                 load8<VEC>(a.w_pre, c0, d, lane, w);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    dn[j][i] = hv[j][i] * w[i];
                     ss[0] = fmaf(xv[j][i], xv[j][i], ss[0]);
-                    ss[1] = fmaf(xv[j][i], dn[j][i], ss[1]);
+                    ss[1] = fmaf(xv[j][i], hv[j][i] * w[i], ss[1]);
                 }
             }
             row_sum<2>(ss, red[1], W, warp, lane);
             const float rx = 1.f / sqrtf(ss[0] * inv_d + a.eps);
-            const float k = ss[1] * inv_d * rx * rx * rx;                 // mean(dn n_x) / rms^2
+            const float k = ss[1] * inv_d * rx * rx;                      // mean(dn n_x) / rms
 #pragma unroll
-            for (int j = 0; j < C; ++j)
+            for (int j = 0; j < C; ++j) {
+                float w[8];
+                load8<VEC>(a.w_pre, (warp + j * W) * kChunk, d, lane, w);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     accP[j][i] = fmaf(hv[j][i], xv[j][i] * rx, accP[j][i]);
-                    dv[j][i] += dn[j][i] * rx - xv[j][i] * k;
+                    dv[j][i] = fmaf(fmaf(hv[j][i], w[i], -xv[j][i] * k), rx, dv[j][i]);
                 }
+            }
         }
 #pragma unroll
         for (int j = 0; j < C; ++j)
@@ -231,15 +289,20 @@ __global__ void __launch_bounds__(32 * kMaxWarps) residual_norm_bwd_kernel(const
 #pragma unroll
             for (int j = 0; j < C; ++j) {
                 const int c0 = (warp + j * W) * kChunk;
-                float w[8], s[8];
+                float w[8];
                 load8<VEC>(a.w_post, c0, d, lane, w);
-                if (a.res_scale) load8<VEC>(a.res_scale, c0, d, lane, s);
+                if (a.res_scale) {
+                    float s[8];
+                    load8<VEC>(a.res_scale, c0, d, lane, s);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] *= s[i];
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float coef = a.res_scale ? w[i] * s[i] : w[i];
-                    accA[j][i] = fmaf(dv[j][i] * gv[j][i], yv[j][i], accA[j][i]);
-                    dv[j][i] *= coef;                                     // D s w_post
-                    ss[0] = fmaf(dv[j][i] * gv[j][i], yv[j][i], ss[0]);
+                    const float t = dv[j][i] * gv[j][i];
+                    accA[j][i] = fmaf(t, yv[j][i], accA[j][i]);
+                    dv[j][i] = t * w[i];                                  // u = D s sigma w_post
+                    ss[0] = fmaf(dv[j][i], yv[j][i], ss[0]);
                 }
             }
             row_sum<1>(ss, red[2], W, warp, lane);
@@ -252,30 +315,23 @@ __global__ void __launch_bounds__(32 * kMaxWarps) residual_norm_bwd_kernel(const
                 float o[8];
                 if (a.gate_mode == MOM_GATE_ELEMENT && b.dgate) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = dv[j][i] * yv[j][i] * gv[j][i] * (1.f - gv[j][i]);
+                    for (int i = 0; i < 8; ++i) o[i] = dv[j][i] * yv[j][i] * (1.f - gv[j][i]);
                     store8<VEC>(reinterpret_cast<T*>(b.dgate) + row * d, c0, d, lane, o);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = (dv[j][i] * gv[j][i] - yv[j][i] * m) * ry;
+                for (int i = 0; i < 8; ++i) o[i] = (dv[j][i] - yv[j][i] * m) * ry;
                 store8<VEC>(reinterpret_cast<T*>(b.dy) + row * d, c0, d, lane, o);
             }
         }
-        // the next row's sums reuse `red`: with three buffers a warp can be at
-        // most one row_sum ahead of the slowest reader of the buffer it writes
+        // the next row's sums reuse `red`
         if (W > 1) __syncthreads();
     }
     float* pa = b.partial + (int64_t)blockIdx.x * 2 * d;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
         const int c0 = (warp + j * W) * kChunk;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = c0 + chunk_col<VEC>(lane, i);
-            if (c < d) {
-                pa[c] = accA[j][i];
-                pa[d + c] = accP[j][i];
-            }
-        }
+        store8<VEC>(pa, c0, d, lane, accA[j]);
+        store8<VEC>(pa + d, c0, d, lane, accP[j]);
     }
 }
 
@@ -314,35 +370,42 @@ int sm_count() {
     return sms;
 }
 
+// Chunks of 256 channels a warp holds.  Forward: two up to 4096 channels (16384
+// rows of 1024, bf16, an element gate: 44 us; one 49 us, four 47 us), four
+// above, so that a row stays within 16 warps.  Adjoint, which holds five
+// operands and two column sums: one up to 2048 channels (104 us; two 122 us),
+// 16 warps an SM (32: 124 us, by spilling its registers).
+constexpr int kFwdC = 2, kBwdC = 1, kBwdWarps = 16;
 template <typename XT, typename T, bool VEC>
 void run_fwd(ResNormArgs a, cudaStream_t st) {
     const int chunks = (int)cdiv(a.d, kChunk);
-    const int C = chunks <= 1 ? 1 : chunks <= 2 ? 2 : 4;
+    const int C = chunks <= 1 ? 1 : chunks <= 8 * kFwdC ? kFwdC : 4;
     const int W = (int)cdiv(chunks, C);
     a.warps_per_row = W;
     const int threads = W > 1 ? 32 * W : 128;
     const int64_t grid = W > 1 ? a.n_rows : cdiv(a.n_rows, threads / 32);
-    if (C == 1) residual_norm_kernel<XT, T, VEC, 1><<<(unsigned)grid, threads, 0, st>>>(a);
-    else if (C == 2) residual_norm_kernel<XT, T, VEC, 2><<<(unsigned)grid, threads, 0, st>>>(a);
-    else residual_norm_kernel<XT, T, VEC, 4><<<(unsigned)grid, threads, 0, st>>>(a);
+    if (C == 1) residual_norm_kernel<XT, T, VEC, 1, 8><<<(unsigned)grid, threads, 0, st>>>(a);
+    else if (C == kFwdC) residual_norm_kernel<XT, T, VEC, kFwdC, 8><<<(unsigned)grid, threads, 0, st>>>(a);
+    else residual_norm_kernel<XT, T, VEC, 4, 16><<<(unsigned)grid, threads, 0, st>>>(a);
 }
 
 template <typename XT, typename T, typename G, bool VEC>
 void run_bwd(const ResNormArgs& a, const ResNormBwdArgs& b, int grid, cudaStream_t st) {
     const int chunks = (int)cdiv(a.d, kChunk);
-    const int C = chunks <= 16 ? 1 : chunks <= 32 ? 2 : 4;
+    const int C = chunks <= 8 * kBwdC ? kBwdC : chunks <= 16 ? 2 : 4;
     const int threads = 32 * (int)cdiv(chunks, C);
-    if (C == 1) residual_norm_bwd_kernel<XT, T, G, VEC, 1><<<grid, threads, 0, st>>>(a, b);
-    else if (C == 2) residual_norm_bwd_kernel<XT, T, G, VEC, 2><<<grid, threads, 0, st>>>(a, b);
-    else residual_norm_bwd_kernel<XT, T, G, VEC, 4><<<grid, threads, 0, st>>>(a, b);
+    if (C == kBwdC) residual_norm_bwd_kernel<XT, T, G, VEC, kBwdC, 8><<<grid, threads, 0, st>>>(a, b);
+    else if (C == 2) residual_norm_bwd_kernel<XT, T, G, VEC, 2, 8><<<grid, threads, 0, st>>>(a, b);
+    else residual_norm_bwd_kernel<XT, T, G, VEC, 4, 16><<<grid, threads, 0, st>>>(a, b);
 }
 
 }  // namespace
 
 // rows of partial column sums the adjoint writes
 int residual_norm_bwd_parts(int64_t n_rows, int d) {
-    const int warps = (int)cdiv(cdiv(d, kChunk), d <= 4096 ? 1 : d <= 8192 ? 2 : 4);
-    const int64_t most = (int64_t)sm_count() * (warps <= 4 ? 16 / warps : warps <= 8 ? 2 : 1);
+    const int chunks = (int)cdiv(d, kChunk);
+    const int warps = (int)cdiv(chunks, chunks <= 8 * kBwdC ? kBwdC : chunks <= 16 ? 2 : 4);
+    const int64_t most = (int64_t)sm_count() * (warps <= kBwdWarps ? kBwdWarps / warps : 1);
     return (int)(n_rows < most ? n_rows : most);
 }
 

@@ -20,25 +20,57 @@ template <bool VEC> __device__ __forceinline__ int chunk_col(int lane, int i) {
     return VEC ? lane * 8 + i : i * 32 + lane;
 }
 
-// 8 channels of a row from channel c0 of the chunk on; channels >= d give 0.
-// With VEC, d is a multiple of 8 and a lane's 8 channels are all in or all out.
-template <bool VEC, typename T>
-__device__ __forceinline__ void load8(const T* row, int c0, int d, int lane, float* out) {
-    if constexpr (VEC) {
-        const int c = c0 + lane * 8;
-        if (c < d) {
-            load_vec<8>(row + c, out);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) out[i] = 0.f;
-        }
-    } else {
+// A lane's 8 channels of a row as they lie in memory (channels >= d give 0):
+// held packed between the load and the use, so that several rows' worth can be
+// in flight.  With VEC, d is a multiple of 8 and a lane's 8 channels are all in
+// or all out.
+template <typename T, bool VEC> struct Raw8 {
+    float v[8];
+    __device__ __forceinline__ void load(const T* row, int c0, int d, int lane) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int c = c0 + i * 32 + lane;
-            out[i] = c < d ? to_f(row[c]) : 0.f;
+            v[i] = c < d ? to_f(row[c]) : 0.f;
         }
     }
+    __device__ __forceinline__ void get(float* out) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[i] = v[i];
+    }
+};
+template <> struct Raw8<bf16, true> {
+    uint4 u;
+    __device__ __forceinline__ void load(const bf16* row, int c0, int d, int lane) {
+        const int c = c0 + lane * 8;
+        u = c < d ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void get(float* out) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            out[2 * i] = __uint_as_float(w[i] << 16);
+            out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+template <> struct Raw8<float, true> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* row, int c0, int d, int lane) {
+        const int c = c0 + lane * 8;
+        a = c < d ? *reinterpret_cast<const float4*>(row + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        b = c < d ? *reinterpret_cast<const float4*>(row + c + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __device__ __forceinline__ void get(float* out) const {
+        out[0] = a.x; out[1] = a.y; out[2] = a.z; out[3] = a.w;
+        out[4] = b.x; out[5] = b.y; out[6] = b.z; out[7] = b.w;
+    }
+};
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void load8(const T* row, int c0, int d, int lane, float* out) {
+    Raw8<T, VEC> r;
+    r.load(row, c0, d, lane);
+    r.get(out);
 }
 template <bool VEC, typename T>
 __device__ __forceinline__ void store8(T* row, int c0, int d, int lane, const float* v) {
@@ -56,49 +88,65 @@ __device__ __forceinline__ void store8(T* row, int c0, int d, int lane, const fl
 
 // --------------------------------------------------- 8-bit checkpoints --
 // A group of 128 channels of a row keeps scale = fl32(max|x| / 127) and the
-// codes round_half_even(x / scale), exactly: the quotient is never formed, a
-// rounded product with 1/scale gives a first code and the remainder
-// x - code * scale (one fused multiply-add; it is a multiple of half an ulp
-// of the scale below 2^24 of them, so it is exact) moves it by one where the
-// product fell on the other side of a border.  A group whose largest
-// magnitude is below 2^-100 is stored as zeros; a group that holds an
-// infinity or a NaN gets a NaN scale, so that all of it restores to NaN.
+// codes round_half_even(x / scale), exactly: the quotient is never formed.  A
+// first code is the rounded product with 1/scale (the addition of 1.5 * 2^23
+// leaves the integer in the low bits); the remainder x - code * scale, one
+// fused multiply-add, is a multiple of half an ulp of the scale below 2^24 of
+// them, so it is exact, and where it reaches half a scale the code moves by one
+// (another code is nearer, or a tie goes to the even one).  That is rare: one
+// test covers a lane's 8 elements.  A group whose largest magnitude is below
+// 2^-100 is stored as zeros; a group that holds an infinity or a NaN gets a NaN
+// scale, so that all of it restores to NaN.
+constexpr float kRoundMagic = 12582912.f;                     // 1.5 * 2^23
+
 __device__ __forceinline__ float act8_scale(uint32_t amax_bits) {
     if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
     const float a = __uint_as_float(amax_bits);
     return a < 7.888609052210118e-31f ? 0.f : a / 127.f;      // 2^-100
 }
-__device__ __forceinline__ int act8_code(float x, float s, float inv) {
-    if (!(s > 0.f)) return 0;
-    float q = rintf(x * inv);
-    const float r = fmaf(-q, s, x), half = 0.5f * s;
-    const bool odd = (static_cast<int>(q) & 1) != 0;
-    if (r > half || (r == half && odd)) q += 1.f;
-    if (r < -half || (r == -half && odd)) q -= 1.f;
-    return static_cast<int>(q);
-}
 
-// The two groups' scales of a chunk held in v (lane layout above): every lane
-// gets the scale of its element i in s[i >= 4] (VEC: both entries are its own
-// group's).
+// The two groups' scales of a chunk held in v (lane layout above): the scale of
+// element i in s[i >= 4] (VEC: both entries are the lane's own group's).
 template <bool VEC> __device__ __forceinline__ void act8_scales(const float* v, float (&s)[2]) {
     uint32_t m[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
-        if constexpr (VEC) m[0] = m[0] > b ? m[0] : b;
-        else m[i >> 2] = m[i >> 2] > b ? m[i >> 2] : b;
+        if constexpr (VEC) m[0] = max(m[0], b);
+        else m[i >> 2] = max(m[i >> 2], b);
     }
     if constexpr (VEC) {
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-            const uint32_t b = __shfl_xor_sync(0xffffffffu, m[0], o);
-            m[0] = m[0] > b ? m[0] : b;
-        }
+        for (int o = 8; o > 0; o >>= 1) m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
         s[0] = s[1] = act8_scale(m[0]);
     } else {
         s[0] = act8_scale(__reduce_max_sync(0xffffffffu, m[0]));
         s[1] = act8_scale(__reduce_max_sync(0xffffffffu, m[1]));
+    }
+}
+
+// The codes of a lane's 8 elements, in the low byte of q[i].
+__device__ __forceinline__ void act8_codes(const float* v, const float (&s)[2], uint32_t* q) {
+    // 1 / scale: at most two ulps off, which the remainder puts right
+    const float inv[2] = {s[0] > 0.f ? __fdividef(1.f, s[0]) : 0.f, s[1] > 0.f ? __fdividef(1.f, s[1]) : 0.f};
+    bool fix = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float f = fmaf(v[i], inv[i >> 2], kRoundMagic);
+        const float r = fmaf(kRoundMagic - f, s[i >> 2], v[i]);
+        q[i] = __float_as_uint(f);
+        fix |= !(fabsf(r) < 0.5f * s[i >> 2]);                // also where the scale is 0 or NaN
+    }
+    if (fix) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float sc = s[i >> 2], half = 0.5f * sc;
+            if (!(sc > 0.f)) { q[i] = 0u; continue; }
+            const float r = fmaf(kRoundMagic - __uint_as_float(q[i]), sc, v[i]);
+            const bool odd = (q[i] & 1u) != 0u;
+            if (r > half || (r == half && odd)) q[i] += 1u;
+            else if (r < -half || (r == -half && odd)) q[i] -= 1u;
+        }
     }
 }
 
@@ -107,56 +155,67 @@ template <bool VEC>
 __device__ __forceinline__ void act8_store(const float* v, int c0, int d, int lane, int8_t* codes_row,
                                            float* scales_row) {
     float s[2];
+    uint32_t q[8];
     act8_scales<VEC>(v, s);
-    const float inv[2] = {s[0] > 0.f ? 1.f / s[0] : 0.f, s[1] > 0.f ? 1.f / s[1] : 0.f};
+    act8_codes(v, s, q);
     const int g0 = c0 / kActGroup;
     if constexpr (VEC) {
         const int c = c0 + lane * 8;
         if (c < d) {
-            uint32_t w[2] = {0u, 0u};
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                w[i >> 2] |= (static_cast<uint32_t>(act8_code(v[i], s[0], inv[0])) & 0xffu) << (8 * (i & 3));
-            *reinterpret_cast<uint2*>(codes_row + c) = make_uint2(w[0], w[1]);
+            const uint32_t lo = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+            const uint32_t hi = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+            *reinterpret_cast<uint2*>(codes_row + c) = make_uint2(lo, hi);
             if ((lane & 15) == 0) scales_row[g0 + (lane >> 4)] = s[0];
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int c = c0 + i * 32 + lane;
-            if (c < d) codes_row[c] = static_cast<int8_t>(act8_code(v[i], s[i >> 2], inv[i >> 2]));
+            if (c < d) codes_row[c] = static_cast<int8_t>(q[i]);
         }
         if (lane == 0 && c0 < d) scales_row[g0] = s[0];
         if (lane == 0 && c0 + kActGroup < d) scales_row[g0 + 1] = s[1];
     }
 }
 
-// The restored values of a chunk: code * scale (one rounding to float32).
-template <bool VEC>
-__device__ __forceinline__ void act8_load(const int8_t* codes_row, const float* scales_row, int c0, int d, int lane,
-                                          float* out) {
-    const int g0 = c0 / kActGroup;
-    if constexpr (VEC) {
+// A lane's 8 restored values, code * scale (one rounding to float32), held
+// packed until they are used.
+struct Q8 {};                  // the stream's type tag where it is a checkpoint
+template <bool VEC> struct Raw8Q;
+template <> struct Raw8Q<true> {
+    uint2 u;
+    float s;
+    __device__ __forceinline__ void load(const int8_t* codes_row, const float* scales_row, int c0, int d, int lane) {
         const int c = c0 + lane * 8;
+        u = make_uint2(0u, 0u);
+        s = 0.f;
         if (c < d) {
-            const uint2 u = *reinterpret_cast<const uint2*>(codes_row + c);
-            const float s = scales_row[g0 + (lane >> 4)];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t w = i < 4 ? u.x : u.y;
-                out[i] = static_cast<float>(static_cast<int8_t>(w >> (8 * (i & 3)))) * s;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) out[i] = 0.f;
+            u = *reinterpret_cast<const uint2*>(codes_row + c);
+            s = scales_row[c0 / kActGroup + (lane >> 4)];
         }
-    } else {
+    }
+    __device__ __forceinline__ void get(float* out) const {
+        // byte + 128 in the low mantissa of 2^23: an exact float of the code
+        const uint32_t w[2] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            out[i] = (__uint_as_float(__byte_perm(w[i >> 2], 0x4b000000u, 0x7440 + (i & 3))) - 8388736.f) * s;
+    }
+};
+template <> struct Raw8Q<false> {
+    float v[8];
+    __device__ __forceinline__ void load(const int8_t* codes_row, const float* scales_row, int c0, int d, int lane) {
+        const int g0 = c0 / kActGroup;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int c = c0 + i * 32 + lane;
-            out[i] = c < d ? static_cast<float>(codes_row[c]) * scales_row[g0 + (i >> 2)] : 0.f;
+            v[i] = c < d ? static_cast<float>(codes_row[c]) * scales_row[g0 + (i >> 2)] : 0.f;
         }
     }
-}
+    __device__ __forceinline__ void get(float* out) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[i] = v[i];
+    }
+};
 
 }  // namespace mom

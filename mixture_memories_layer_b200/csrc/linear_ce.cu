@@ -2,33 +2,49 @@
 // its gradient, on the tcgen05 tensor cores without storing the logits.
 //
 //   forward   lse_t = log sum_v exp(z_tv),  loss_t = lse_t - z_t,target
-//   backward  g_tv = r_t (exp(z_tv - lse_t) - [v = target_t]),
-//             dx = g W,  dW = g^T x
+//   backward  g_tv = exp(z_tv - lse_t) - [v = target_t],
+//             (times the row's weight),  dx = r g W,  dW = r g^T x
 //
 // One persistent GEMM kernel runs all four products; they differ in the
 // operands' majors and in what happens to an accumulator tile:
-//   stats  x W^T      each row's running maximum and sum of exponentials over
+//   STATS  x W^T      each row's running maximum and sum of exponentials over
 //                     the tile's columns (float32, one pass over TMEM), and
 //                     the target's logit; logsumexp_kernel joins the tiles
-//   grad   x W^T      the logits of one piece of the vocabulary again, made
+//   GRAD   x W^T      the logits of one piece of the vocabulary again, made
 //                     into g and stored as bf16
-//   store / add       dx += g W over the pieces (float32, added in L2 by the
-//                     copy engine, in piece order), dW = g^T x
+//   OUT    g W, g^T x both products of a piece in one launch
+// Rows without a target take no part in the gradient: gather_kernel packs the
+// rows that have one, in order, and the later kernels read their number on the
+// device, so a batch that is mostly padding costs what its targets cost.
+//
+// The common factor r (1 / rows for the mean loss) multiplies the sums, in
+// float32, as they are stored: in a bf16 g it would give every -1 of g the
+// same relative error, up to 2^-8 of the whole gradient (16384 rows, 32000
+// classes: 0.0030 of the gradient's norm, and 0.0017, the output's own
+// rounding, without).  Weights that differ from row to row are in g.
+//
 // Bound by the tensor cores (2 n d v operations a product) except for few
-// rows, where reading W once bounds it; then the long vocabulary axis of dx
-// (or the long token axis of dW) is split over CTAs and the slots are summed
-// in a fixed order.  There are no atomics on floats: results repeat.
+// rows, where reading W once bounds it.  dx and dW of a piece have few, long
+// tiles; schedule() deals them out so that the clusters finish together, and
+// an axis so long that one tile would outlast the rest is split into slots
+// that join_kernel adds in order.  No atomics on floats: results repeat.
 //
 // float32 operands: every value is split exactly into three bf16 parts, a =
 // a0 + a1 + a2 (8 bits each), and the six products a_i b_j with i + j <= 2 run
-// as one longer K loop into the same accumulator, smallest first; the rest is
-// below 2^-24 of a product.
+// into the same accumulator, smallest first; the rest is below 2^-24 of a
+// product.  The tensor core truncates as it accumulates, so a float32 tile's
+// sum leaves TMEM every 128 of K and is continued in registers, rounded.
 //
-// Roles (320 threads, one CTA per SM, persistent over tiles): warp 0 issues
-// the TMA loads of both operands (4 stages of 128 x 64 and 256 x 64), warp 1
-// the MMAs (M 128, N 256, K 16) into one of two TMEM accumulators, warps 2-9
-// are the epilogue (two warps a TMEM lane quarter) and overlap the next
-// tile's main loop.  Every wait is bounded (sm100.cuh).
+// Two CTAs of a cluster share a 256 x 256 tile (cta_group::2, K 16 an
+// instruction): each loads its 128 rows of A and half of B, 64 bytes from L2
+// for each tensor-core cycle where a CTA by itself (128 x 256) needs 96.
+// Roles (320 threads): warp 0 issues the TMA loads (6 stages of K 64; float32
+// 2 stages of all three parts), warp 1 of the first CTA the MMAs into one of
+// two TMEM accumulators, warps 2-9 are the epilogue (two warps a TMEM lane
+// quarter) and overlap the next tile's main loop.  Every wait is bounded
+// (sm100.cuh).
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -39,32 +55,49 @@ namespace {
 
 using namespace sm100;
 
-constexpr int BM = 128, BN = 256, BK = 64, STAGES = 4;
-constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2;
+constexpr int BM = 256, BN = 256, BK = 64;           // a cluster's tile
+constexpr int HM = BM / 2;                           // a CTA's rows of A, and of B
+constexpr int OP_BYTES = HM * BK * 2;                // one operand part of a stage
 constexpr int MN_GROUP = 64 * BK * 2;                // an MN-major box: 64 MN x 64 K, bf16
 constexpr int NEPI = 256, THREADS = 64 + NEPI;
+constexpr int EPI_ARRIVE = 2 * NEPI / 32;            // warps of both CTAs that free an accumulator
 constexpr int PIECE = 32 * 128;                      // an epilogue warp's staging: 32 rows x 128 bytes
-constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * (A_BYTES + B_BYTES) + (size_t)(NEPI / 32) * PIECE + 256;
 constexpr uint32_t TMEM_COLS = 2 * BN;
+constexpr int SEG_KB = 2;                            // float32: K blocks between two reads of the accumulator
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+template <int PARTS> struct Stages { static constexpr int N = PARTS == 1 ? 6 : 2, BYTES = 2 * PARTS * OP_BYTES; };
+template <int PARTS> constexpr size_t smem_bytes() {
+    return 1024 + (size_t)Stages<PARTS>::N * Stages<PARTS>::BYTES + (size_t)(NEPI / 32) * PIECE + 256;
+}
 
-enum Epi { EPI_STATS, EPI_GRAD, EPI_BF16, EPI_F32 };
+enum Epi { EPI_STATS, EPI_GRAD, EPI_OUT };
+
+// One of OUT's products: [rows, d] over kb blocks of K, its slots, and where
+// the result goes.
+struct Prod {
+    int64_t rows, row0;                  // output rows of the piece, the first one's place in `out`
+    int kb, slots;
+    void* out;
+    const int32_t* row_of;               // row -> output row (null: row0 + row)
+    const float* scale;                  // r (null: 1)
+    float* partial;                      // [slots][up(rows, 32) / 32][up(d, 32)][32], null: none
+    int add, last;                       // add to what the partial holds; this is the last piece
+};
 
 struct GemmArgs {
-    int64_t m_tiles, n_tiles, tiles;     // output tiles; tiles = m_tiles * n_tiles * k_splits
-    int kb_total, kb_split;              // K blocks of 64 in all and of one split
-    int n_pairs;                         // products of operand parts
-    uint8_t pa[6], pb[6];
-    int b_row0;                          // K-major B: first row; MN-major B: first K row
-    int64_t m, n;                        // valid output rows and columns
-    // stats / grad
+    int64_t rows, cols;                  // STATS, GRAD: rows of x, classes of the piece
+    int kb;                              // K blocks of d
+    int b_row0;                          // W's first row
+    const int32_t* live;                 // GRAD, OUT: number of packed rows (device)
     const int32_t* targets;
     int64_t v0, vocab;                   // the piece's first class
-    float2* partials;                    // [column half tiles][m]
+    float2* partials;                    // [column half tiles][rows]
     float* zt;                           // the targets' logits
-    const float *lse, *dloss, *dscale;
-    int n_parts;                         // bf16 parts of g
-    int add;                             // EPI_F32: add to what is there
+    const float *lse2, *weight;          // GRAD: log2(e) lse of the packed rows, their weights (null: 1)
+    int32_t* ticket;                     // STATS: set to 0 for logsumexp_kernel
+    // OUT: dx (rows and K of dw follow `live`), dw
+    Prod dx, dw;
+    int d, bn, vec;                      // bn: columns of a tile; vec: out's rows take 16-byte stores
     void* ws;
 };
 
@@ -75,11 +108,6 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
-                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1), "r"(c2)
-                 : "memory");
-}
-__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
-    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];"
                  ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
 }
@@ -96,341 +124,633 @@ __device__ __forceinline__ float bf16_part(float v, int p) {
     return v;
 }
 
+// ------------------------------------------------------- CTA pairs --
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address of this CTA's `addr` in the cluster's first CTA
+__device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// a box of this CTA's shared memory, counted on a barrier of either CTA
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                             int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void pair_umma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// arrives on the barrier at this offset in both CTAs when the MMAs so far are done
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(bar), "h"((uint16_t)3)
+        : "memory");
+}
+
+// ---------------------------------------------------------- scheduling --
 struct Tile {
+    int dw;                              // OUT: the product
     int64_t mt, nt;
     int ks, kb0, kb1;
 };
-// rows fastest: the CTAs of one wave share few column tiles of B
-__device__ __forceinline__ Tile tile_at(const GemmArgs& p, int64_t t) {
-    Tile T;
-    T.mt = t % p.m_tiles;
-    const int64_t r = t / p.m_tiles;
-    T.nt = r % p.n_tiles;
-    T.ks = (int)(r / p.n_tiles);
-    T.kb0 = T.ks * p.kb_split;
-    T.kb1 = T.kb0 + p.kb_split < p.kb_total ? T.kb0 + p.kb_split : p.kb_total;
-    return T;
+
+// Tile j of cluster c among n; false past its last one.  OUT: the product with
+// the longer tiles first, round robin; the clusters that got one fewer take
+// the head start of as many of the other's tiles as last as long as one, and
+// the rest goes round robin, those clusters first.  Closed form, so that every
+// role walks the same list.
+struct Schedule {
+    int64_t c, n, m1, m2, n_tiles, na, nb, head, first;
+    int kb1, kb2, k1, k2, dw_first;
+    __device__ __forceinline__ Schedule(const GemmArgs& p, int epi) {
+        c = blockIdx.x >> 1;
+        n = gridDim.x >> 1;
+        const int64_t live = p.live ? *p.live : p.rows;
+        m1 = cdiv(live, BM);
+        dw_first = 0;
+        if (epi != EPI_OUT) {
+            n_tiles = cdiv(p.cols, BN);
+            na = m1 * n_tiles;
+            k1 = p.kb;
+            return;
+        }
+        n_tiles = cdiv(p.d, p.bn);
+        m2 = cdiv(p.dw.rows, BM);
+        kb1 = p.dx.kb;
+        kb2 = (int)cdiv(live, BK);
+        k1 = (int)cdiv(kb1, p.dx.slots);
+        k2 = (int)cdiv(kb2, p.dw.slots);
+        dw_first = k2 > k1;
+        const int64_t n1 = m1 * n_tiles * p.dx.slots, n2 = m2 * n_tiles * p.dw.slots;
+        na = dw_first ? n2 : n1;
+        nb = dw_first ? n1 : n2;
+        first = na % n;                            // clusters that get one more
+        // (an epilogue lasts about 4 K blocks)
+        head = first ? (dw_first ? (k2 + 4) / (k1 + 4) : (k1 + 4) / (k2 + 4)) : 0;
+    }
+    __device__ __forceinline__ bool at(int epi, int64_t j, Tile& T) const {
+        int64_t t = c + j * n;
+        if (epi != EPI_OUT) {
+            T.dw = 0;
+            T.ks = 0;
+            T.kb0 = 0;
+            T.kb1 = k1;
+            if (t >= na) return false;
+            T.mt = t % m1;                         // rows fastest: a wave shares few column tiles of W
+            T.nt = t / m1;
+            return true;
+        }
+        T.dw = dw_first;
+        if (t >= na) {
+            T.dw = 1 - dw_first;
+            const int64_t light = n - first, i = j - (na / n + (c < first ? 1 : 0));
+            if (c >= first && i < head) t = i * light + (c - first);
+            else t = head * light + (c >= first ? (i - head) * n + (c - first) : i * n + light + c);
+            if (t >= nb) return false;
+        }
+        T.nt = t % n_tiles;
+        const int64_t r = t / n_tiles, m = T.dw ? m2 : m1;
+        const int k = T.dw ? k2 : k1, kb = T.dw ? kb2 : kb1;
+        T.mt = r % m;
+        T.ks = (int)(r / m);
+        T.kb0 = T.ks * k;
+        T.kb1 = T.kb0 + k < kb ? T.kb0 + k : kb;
+        return true;
+    }
+};
+
+// ------------------------------------------------------------- outputs --
+// 32 columns of 32 rows (lane = row, v = its columns from `col` on) to the
+// rows `row` (< 0: none) of out [.., d]: through the warp's staging, so that
+// the rows are written in whole sectors.
+template <typename T>
+__device__ __forceinline__ void emit(T* out, int d, bool vec, int64_t row, int64_t col, const float* v, uint32_t piece,
+                                     int lane) {
+    constexpr int Q = 2 * sizeof(T);               // 16-byte chunks of a row
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const uint32_t at = piece + lane * (16 * Q) + ((sizeof(T) == 4 ? q ^ (lane & 7) : q ^ ((lane >> 1) & 3)) << 4);
+        if constexpr (sizeof(T) == 4)
+            st_shared_v4(at, __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                         __float_as_uint(v[4 * q + 3]));
+        else
+            st_shared_v4(at, pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
+                         pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7]));
+    }
+    __syncwarp();
+    constexpr int E = 16 / sizeof(T);              // elements of a chunk
+    if (vec) {
+        constexpr int RI = 32 / Q;                 // rows an iteration
+        const int q = lane % Q;
+#pragma unroll
+        for (int it = 0; it < Q; ++it) {
+            const int r = it * RI + lane / Q;
+            const int64_t to = __shfl_sync(0xffffffffu, row, r);
+            uint32_t a, b, c, e;
+            const uint32_t at = piece + r * (16 * Q) + ((sizeof(T) == 4 ? q ^ (r & 7) : q ^ ((r >> 1) & 3)) << 4);
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(e) : "r"(at) : "memory");
+            if (to >= 0 && col + q * E < d) *reinterpret_cast<uint4*>(out + to * d + col + q * E) = make_uint4(a, b, c, e);
+        }
+    } else {
+        const int q = lane / E;
+#pragma unroll 4
+        for (int r = 0; r < 32; ++r) {
+            const int64_t to = __shfl_sync(0xffffffffu, row, r);
+            const uint32_t at = piece + r * (16 * Q) +
+                                ((sizeof(T) == 4 ? q ^ (r & 7) : q ^ ((r >> 1) & 3)) << 4) + (lane % E) * sizeof(T);
+            if (to < 0 || col + lane >= d) continue;
+            if constexpr (sizeof(T) == 4) {
+                uint32_t a;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a) : "r"(at) : "memory");
+                out[to * d + col + lane] = __uint_as_float(a);
+            } else {
+                uint16_t a;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(a) : "r"(at) : "memory");
+                reinterpret_cast<uint16_t*>(out)[to * d + col + lane] = a;
+            }
+        }
+    }
 }
 
-template <int EPI, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(THREADS, 1)
+// A partial's element of row block rb, column col, lane 0.
+__device__ __forceinline__ float* partial_at(const Prod& q, int d, int slot, int64_t rb, int64_t col) {
+    const int64_t blocks = cdiv(q.rows, 32), dp = cdiv(d, 32) * 32;
+    return q.partial + ((slot * blocks + rb) * dp + col) * 32;
+}
+
+template <int PARTS, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-               const __grid_constant__ CUtensorMap tm_out, const GemmArgs p) {
+               const __grid_constant__ CUtensorMap tm_a2, const __grid_constant__ CUtensorMap tm_b2,
+               const GemmArgs p) {
+    constexpr int STAGES = Stages<PARTS>::N, STAGE_BYTES = Stages<PARTS>::BYTES;
+    constexpr bool SEG = PARTS == 3;
+    typedef typename std::conditional<PARTS == 1, bf16, float>::type OT;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = align1024_shared(smem_raw);
-    unsigned char* sA = smem;
-    unsigned char* sB = smem + STAGES * A_BYTES;
-    unsigned char* sOut = sB + STAGES * B_BYTES;
+    unsigned char* sOut = smem + STAGES * STAGE_BYTES;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + (NEPI / 32) * PIECE);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES);
     const uint32_t tfull0 = smem_u32(bars + 2 * STAGES), tempty0 = smem_u32(bars + 2 * STAGES + 2);
     const uint32_t done_bar = smem_u32(bars + 2 * STAGES + 4);
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full0 + 8 * s, 1);
+            mbar_init(full0 + 8 * s, 1);           // of the first CTA: both CTAs' loads
             mbar_init(empty0 + 8 * s, 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull0 + 8 * a, 1);
-            mbar_init(tempty0 + 8 * a, NEPI);
+            mbar_init(tempty0 + 8 * a, EPI_ARRIVE);      // of the first CTA: both epilogues
         }
         mbar_init(done_bar, 1);
         *abort_flag = 0;
         fence_barrier_init();
+        if (EPI == EPI_STATS && p.ticket && blockIdx.x == 0) *p.ticket = 0;
     }
-    if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
-        tmem_relinquish();
-    }
+    if (warp == 1) pair_tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();                                // the other CTA's barriers are ready
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    const Schedule S(p, EPI);
+    Tile T;
 
     if (warp == 0) {
         if (lane == 0) {
             // ---------------------------------------------------- TMA loads
+            const uint32_t full_lead = leader_addr(full0);
+            const int groups = EPI == EPI_OUT ? p.bn / 128 : 2;
+            const uint32_t stage_tx = 2 * PARTS * (OP_BYTES + (EPI == EPI_OUT ? groups * MN_GROUP : OP_BYTES));
             uint32_t it = 0;
             bool ok = true;
-            for (int64_t t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
-                const Tile T = tile_at(p, t);
-                const int m0 = (int)(T.mt * BM), n0 = (int)(T.nt * BN);
-                for (int pr = 0; pr < p.n_pairs && ok; ++pr) {
-                    const int qa = p.pa[pr], qb = p.pb[pr];
-                    for (int kb = T.kb0; kb < T.kb1; ++kb, ++it) {
-                        const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
-                        if (!mbar_wait(empty0 + 8 * s, ph ^ 1, abort_flag, p.ws, 1)) { ok = false; break; }
-                        const uint32_t bar = full0 + 8 * s;
-                        const uint32_t a0 = smem_u32(sA + s * A_BYTES), b0 = smem_u32(sB + s * B_BYTES);
-                        mbar_arrive_expect_tx(bar, A_BYTES + B_BYTES);
-                        if constexpr (A_MN) {
+            for (int64_t j = 0; ok && S.at(EPI, j, T); ++j) {
+                const int m0 = (int)(T.mt * BM) + HM * rank;
+                const int n0 = EPI == EPI_OUT ? (int)(T.nt * p.bn + p.bn / 2 * rank) : (int)(T.nt * BN) + HM * (int)rank;
+                for (int kb = T.kb0; kb < T.kb1; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
+                    if (!mbar_wait(empty0 + 8 * s, ph ^ 1, abort_flag, p.ws, 1)) { ok = false; break; }
+                    if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, stage_tx);
+                    const uint32_t bar = full_lead + 8 * s;
+                    const uint32_t a0 = smem_u32(smem + s * STAGE_BYTES), b0 = a0 + PARTS * OP_BYTES;
 #pragma unroll
-                            for (int g = 0; g < BM / 64; ++g)
-                                tma_load_3d(a0 + g * MN_GROUP, &tm_a, bar, m0 + 64 * g, kb * BK, qa);
+                    for (int q = 0; q < PARTS; ++q) {
+                        if constexpr (EPI == EPI_OUT) {
+                            if (T.dw) {
+                                pair_load_3d(a0 + q * OP_BYTES, &tm_a2, bar, m0, kb * BK, q);
+                                pair_load_3d(a0 + q * OP_BYTES + MN_GROUP, &tm_a2, bar, m0 + 64, kb * BK, q);
+                                for (int g = 0; g < groups; ++g)
+                                    pair_load_3d(b0 + q * OP_BYTES + g * MN_GROUP, &tm_b2, bar, n0 + 64 * g, kb * BK, q);
+                            } else {
+                                pair_load_3d(a0 + q * OP_BYTES, &tm_a, bar, kb * BK, m0, q);
+                                for (int g = 0; g < groups; ++g)
+                                    pair_load_3d(b0 + q * OP_BYTES + g * MN_GROUP, &tm_b, bar, n0 + 64 * g,
+                                                 p.b_row0 + kb * BK, q);
+                            }
                         } else {
-                            tma_load_3d(a0, &tm_a, bar, kb * BK, m0, qa);
-                        }
-                        if constexpr (B_MN) {
-#pragma unroll
-                            for (int g = 0; g < BN / 64; ++g)
-                                tma_load_3d(b0 + g * MN_GROUP, &tm_b, bar, n0 + 64 * g, p.b_row0 + kb * BK, qb);
-                        } else {
-                            tma_load_3d(b0, &tm_b, bar, kb * BK, p.b_row0 + n0, qb);
+                            pair_load_3d(a0 + q * OP_BYTES, &tm_a, bar, kb * BK, m0, q);
+                            pair_load_3d(b0 + q * OP_BYTES, &tm_b, bar, kb * BK, p.b_row0 + n0, q);
                         }
                     }
                 }
             }
-            if (!ok)      // loads still in flight must land before the CTA exits
+            if (!ok && rank == 0)      // loads still in flight must land before the CTAs exit
                 for (uint32_t j = it >= STAGES ? it - STAGES : 0; j < it; ++j)
                     mbar_wait_drain(full0 + 8 * (j % STAGES), (j / STAGES) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             // --------------------------------------------------- MMA issuer
-            constexpr uint32_t IDESC = idesc_bf16_f32(BM, BN, A_MN, B_MN);
+            const int bn = EPI == EPI_OUT ? p.bn : BN;
             uint32_t it = 0, tc = 0;
             bool ok = true;
-            for (int64_t t = blockIdx.x; t < p.tiles && ok; t += gridDim.x, ++tc) {
-                const Tile T = tile_at(p, t);
-                const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
-                if (!mbar_wait(tempty0 + 8 * acc, aph ^ 1, abort_flag, p.ws, 2)) break;
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + acc * BN;
-                const int steps = (T.kb1 - T.kb0) * p.n_pairs;
-                for (int k = 0; k < steps; ++k, ++it) {
-                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
-                    if (!mbar_wait(full0 + 8 * s, ph, abort_flag, p.ws, 3)) { ok = false; break; }
+            for (int64_t j = 0; ok && S.at(EPI, j, T); ++j) {
+                const bool a_mn = EPI == EPI_OUT && T.dw;
+                const uint32_t idesc = idesc_bf16_f32(BM, bn, a_mn, EPI == EPI_OUT);
+                const int seg = SEG ? SEG_KB : T.kb1 - T.kb0;
+                for (int k0 = T.kb0; ok && k0 < T.kb1; k0 += seg, ++tc) {
+                    const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
+                    if (!mbar_wait(tempty0 + 8 * acc, aph ^ 1, abort_flag, p.ws, 2)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(sA + s * A_BYTES), b0 = smem_u32(sB + s * B_BYTES);
+                    const uint32_t d_tmem = tmem_base + acc * BN;
+                    const int k1 = k0 + seg < T.kb1 ? k0 + seg : T.kb1;
+                    for (int kb = k0; kb < k1; ++kb, ++it) {
+                        const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
+                        if (!mbar_wait(full0 + 8 * s, ph, abort_flag, p.ws, 3)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t a0 = smem_u32(smem + s * STAGE_BYTES), b0 = a0 + PARTS * OP_BYTES;
+                        constexpr int PAIRS = PARTS == 1 ? 1 : 6;
+                        constexpr int PA[6] = {PARTS == 1 ? 0 : 2, 1, 0, 1, 0, 0}, PB[6] = {0, 1, 2, 0, 1, 0};
 #pragma unroll
-                    for (int j = 0; j < BK / 16; ++j) {
-                        const uint64_t da = A_MN ? desc_mnmajor_sw128(a0 + 2048 * j, MN_GROUP)
-                                                 : desc_kmajor_sw128(a0 + 32 * j);
-                        const uint64_t db = B_MN ? desc_mnmajor_sw128(b0 + 2048 * j, MN_GROUP)
-                                                 : desc_kmajor_sw128(b0 + 32 * j);
-                        umma_f16(d_tmem, da, db, IDESC, (k | j) != 0);
+                        for (int pr = 0; pr < PAIRS; ++pr) {
+#pragma unroll
+                            for (int i = 0; i < BK / 16; ++i) {
+                                const uint32_t a = a0 + PA[pr] * OP_BYTES, b = b0 + PB[pr] * OP_BYTES;
+                                const uint64_t da = a_mn ? desc_mnmajor_sw128(a + 2048 * i, MN_GROUP)
+                                                         : desc_kmajor_sw128(a + 32 * i);
+                                const uint64_t db = EPI == EPI_OUT ? desc_mnmajor_sw128(b + 2048 * i, MN_GROUP)
+                                                                   : desc_kmajor_sw128(b + 32 * i);
+                                pair_umma(d_tmem, da, db, idesc, kb != k0 || (pr | i) != 0);
+                            }
+                        }
+                        pair_commit(empty0 + 8 * s);
                     }
-                    umma_commit(empty0 + 8 * s);
+                    if (ok) pair_commit(tfull0 + 8 * acc);
                 }
-                if (!ok) break;
-                umma_commit(tfull0 + 8 * acc);
             }
-            // every MMA this CTA issued has finished before TMEM is released
-            umma_commit(done_bar);
+            // every MMA of the pair has finished before TMEM is released
+            pair_commit(done_bar);
             mbar_wait_drain(done_bar, 0);
         }
     } else {
         // ------------------------------------------------------- epilogue
-        // warp 2 + e: TMEM lanes 32 (warp % 4) .. + 31, columns [128 (e / 4), + 128)
+        // warp 2 + e: TMEM lanes 32 (warp % 4) .. + 31, half e / 4 of the tile's columns
         const int e = warp - 2, qd = warp & 3, hf = e >> 2;
-        constexpr int HALF = BN / 2;
+        const int half = EPI == EPI_OUT ? p.bn / 2 : BN / 2;
         const uint32_t piece = smem_u32(sOut + e * PIECE);
-        float gscale = 1.f;
-        if constexpr (EPI == EPI_GRAD) gscale = p.dscale ? *p.dscale : 1.f;
+        const uint32_t lead_tempty = leader_addr(tempty0);
+        const int64_t live = p.live ? *p.live : p.rows;
         uint32_t tc = 0;
-        for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x, ++tc) {
-            const Tile T = tile_at(p, t);
-            const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
-            const int64_t row = T.mt * BM + 32 * qd + lane;
-            const bool live = row < p.m;
-            const int64_t col0 = T.nt * BN + hf * HALF;
-            // the target's column inside this half tile (< 0: not here)
-            int tl = -1;
-            float lse2 = 0.f, wt = 0.f;
-            if constexpr (EPI == EPI_STATS || EPI == EPI_GRAD) {
-                if (live) {
-                    const int64_t tg = p.targets[row];
-                    const bool in = tg >= 0 && tg < p.vocab;
-                    const int64_t rel = tg - p.v0 - col0;
-                    if (in && rel >= 0 && rel < HALF) tl = (int)rel;
+        bool ok = true;
+        for (int64_t j = 0; S.at(EPI, j, T); ++j) {
+            const int64_t row = T.mt * BM + HM * rank + 32 * qd + lane;
+            const int64_t col0 = EPI == EPI_OUT ? T.nt * p.bn + hf * half : T.nt * BN + hf * half;
+            int tl = -1;                           // the target's column inside this half tile (< 0: not here)
+            float lse2 = 0.f, wt = 1.f;
+            if constexpr (EPI != EPI_OUT) {
+                if (row < live) {
+                    const int64_t tg = p.targets[row], rel = tg - p.v0 - col0;
+                    if (tg >= 0 && tg < p.vocab && rel >= 0 && rel < half) tl = (int)rel;
                     if constexpr (EPI == EPI_GRAD) {
-                        if (in) wt = (p.dloss ? p.dloss[row] : 1.f) * gscale;
-                        lse2 = in ? p.lse[row] * kLog2e : INFINITY;      // padding: every exponential is 0
+                        lse2 = p.lse2[row];
+                        if (p.weight) wt = p.weight[row];
                     }
                 }
             }
-            if (!mbar_wait(tfull0 + 8 * acc, aph, abort_flag, p.ws, 4)) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem_base + ((uint32_t)(32 * qd) << 16) + acc * BN + hf * HALF;
-            const int64_t left = p.n - col0;
-            const int nv = left < 0 ? 0 : left < HALF ? (int)left : HALF;      // valid columns of the half tile
-            if constexpr (EPI == EPI_STATS) {
-                float m = -INFINITY, s = 0.f, zt = 0.f;
+            // float32: the tile's sum, continued in registers
+            float sum[SEG ? 128 : 1];
+            uint32_t acc = tc & 1;
+            if constexpr (SEG) {
 #pragma unroll
-                for (int c = 0; c < HALF; c += 32) {
+                for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+                for (int k0 = T.kb0; k0 < T.kb1; k0 += SEG_KB, ++tc) {
+                    acc = tc & 1;
+                    if (!mbar_wait(tfull0 + 8 * acc, (tc >> 1) & 1, abort_flag, p.ws, 4)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t ta = tmem_base + ((uint32_t)(32 * qd) << 16) + acc * BN + hf * half;
+#pragma unroll
+                    for (int c = 0; c < 128; c += 32) {
+                        if (c < half) {
+                            uint32_t r[32];
+                            tmem_ld_x32(ta + c, r);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(r[i]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(lead_tempty + 8 * acc);
+                }
+            } else if (T.kb0 < T.kb1) {
+                ok = mbar_wait(tfull0 + 8 * acc, (tc >> 1) & 1, abort_flag, p.ws, 4);
+                tc_fence_after();
+            }
+            if (!ok) break;
+            const uint32_t taddr = tmem_base + ((uint32_t)(32 * qd) << 16) + acc * BN + hf * half;
+            // columns c .. c + 31 of the half tile (an empty K range: zeros)
+            auto chunk = [&](int c, float* v) {
+                if constexpr (SEG) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = sum[c + i];
+                } else {
                     uint32_t r[32];
                     tmem_ld_x32(taddr + c, r);
                     tmem_ld_wait();
-                    if (c + 32 > nv) {
+                    const bool any = T.kb0 < T.kb1;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i >= nv) r[i] = 0xff800000u;               // -inf
-                    }
-                    float mx = m;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
-                    // all -inf so far: exponentials of (-inf - 0) are 0, not NaN
-                    const float sub = mx == -INFINITY ? 0.f : mx * kLog2e;
-                    s *= ex2(fmaf(m, kLog2e, -sub));
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) s += ex2(fmaf(__uint_as_float(r[i]), kLog2e, -sub));
-                    m = mx;
-                    if (tl >= c && tl < c + 32) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (tl == c + i) zt = __uint_as_float(r[i]);
-                    }
+                    for (int i = 0; i < 32; ++i) v[i] = EPI != EPI_OUT || any ? __uint_as_float(r[i]) : 0.f;
                 }
-                if (live) {
-                    p.partials[(T.nt * 2 + hf) * p.m + row] = make_float2(m, s);
-                    if (tl >= 0) p.zt[row] = zt;
+            };
+            if constexpr (EPI == EPI_OUT) {
+                const Prod& q = T.dw ? p.dw : p.dx;
+                const int64_t rows = T.dw ? q.rows : live;
+                const bool final = q.last && q.slots == 1;
+                int64_t to = -1;
+                float f = 1.f;
+                if (final && row < rows) {
+                    to = q.row_of ? q.row_of[row] : q.row0 + row;
+                    f = q.scale ? *q.scale : 1.f;
                 }
-            } else if constexpr (EPI == EPI_F32) {
+                const int64_t rb = T.mt * (BM / 32) + (HM / 32) * rank + qd;
 #pragma unroll
-                for (int c = 0; c < HALF; c += 32) {
-                    if (c >= nv) break;
-                    if (lane == 0) bulk_wait_read0();          // the previous piece has left shared memory
-                    __syncwarp();
-                    uint32_t r[32];
-                    tmem_ld_x32(taddr + c, r);
-                    tmem_ld_wait();
+                for (int c = 0; c < 128; c += 32) {
+                    if (c < half && col0 + c < p.d && rb * 32 < rows) {
+                        float v[32];
+                        chunk(c, v);
+                        if (q.partial) {
+                            float* at = partial_at(q, p.d, T.ks, rb, col0 + c) + lane;
+                            if (q.add) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        st_shared_v4(piece + lane * 128 + ((q ^ (lane & 7)) << 4), r[4 * q], r[4 * q + 1], r[4 * q + 2],
-                                     r[4 * q + 3]);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && T.mt * BM + 32 * qd < p.m) {
-                        if (p.add) tma_add_3d(&tm_out, piece, (int)col0 + c, (int)(T.mt * BM) + 32 * qd, T.ks);
-                        else tma_store_3d(&tm_out, piece, (int)col0 + c, (int)(T.mt * BM) + 32 * qd, T.ks);
-                        bulk_commit();
+                                for (int i = 0; i < 32; ++i) v[i] += at[i * 32];
+                            }
+                            if (!final) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) at[i * 32] = v[i];
+                            }
+                        }
+                        if (final) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] *= f;
+                            emit(reinterpret_cast<OT*>(q.out), p.d, p.vec != 0, to, col0 + c, v, piece, lane);
+                        }
                     }
                 }
             } else {
-                const int parts = EPI == EPI_GRAD ? p.n_parts : 1;
-                // g is stored over whole tiles (0 past the vocabulary); a bf16
-                // output only where it has columns
-                const int ncol = EPI == EPI_GRAD ? HALF : nv;
-                for (int part = 0; part < parts; ++part) {
+                const int64_t left = p.cols - col0;
+                const int nv = left < 0 ? 0 : left < half ? (int)left : half;      // valid columns of the half tile
+                if constexpr (EPI == EPI_STATS) {
+                    float m = -INFINITY, s = 0.f, zt = 0.f;
 #pragma unroll
-                    for (int pc = 0; pc < HALF / 64; ++pc) {
-                        if (pc * 64 >= ncol) break;
-                        if (lane == 0) bulk_wait_read0();
-                        __syncwarp();
+                    for (int c = 0; c < 128; c += 32) {
+                        float v[32];
+                        chunk(c, v);
+                        if (c + 32 > nv) {
 #pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {
-                            const int c = pc * 64 + hh * 32;
-                            uint32_t r[32], w[16];
-                            tmem_ld_x32(taddr + c, r);
-                            tmem_ld_wait();
-                            if constexpr (EPI == EPI_GRAD) {
+                            for (int i = 0; i < 32; ++i)
+                                if (c + i >= nv) v[i] = -INFINITY;
+                        }
+                        float mx = m;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, v[i]);
+                        // all -inf so far: exponentials of (-inf - 0) are 0, not NaN
+                        const float sub = mx == -INFINITY ? 0.f : mx * kLog2e;
+                        s *= ex2(fmaf(m, kLog2e, -sub));
+                        float s2 = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            s += ex2(fmaf(v[i], kLog2e, -sub));
+                            s2 += ex2(fmaf(v[i + 1], kLog2e, -sub));
+                        }
+                        s += s2;
+                        m = mx;
+                        if (tl >= c && tl < c + 32) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (tl == c + i) zt = v[i];
+                        }
+                    }
+                    if (row < live) {
+                        p.partials[(T.nt * 2 + hf) * p.rows + row] = make_float2(m, s);
+                        if (tl >= 0) p.zt[row] = zt;
+                    }
+                } else {
+                    // g is 0 past the vocabulary and past the packed rows
+                    const int nvr = row < live ? nv : 0;
+                    const bool some = T.mt * BM + HM * rank + 32 * qd < cdiv(live, BK) * BK;   // whole K blocks of dW
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part) {
+#pragma unroll
+                        for (int pc = 0; pc < 2; ++pc) {
+                            if (lane == 0) bulk_wait_read0();      // the previous piece has left shared memory
+                            __syncwarp();
+#pragma unroll
+                            for (int hh = 0; hh < 2; ++hh) {
+                                const int c = pc * 64 + hh * 32;
                                 float g[32];
+                                chunk(c, g);
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) {
-                                    const float pv = ex2(fmaf(__uint_as_float(r[i]), kLog2e, -lse2));
-                                    g[i] = c + i < nv ? wt * (tl == c + i ? pv - 1.f : pv) : 0.f;
-                                }
-                                if (lse2 == INFINITY) {        // padding, whatever its logits are
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) g[i] = 0.f;
-                                }
-                                if (part > 0) {
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) g[i] = bf16_part(g[i], part);
+                                    const float pv = ex2(fmaf(g[i], kLog2e, -lse2));
+                                    g[i] = c + i < nvr ? wt * (tl == c + i ? pv - 1.f : pv) : 0.f;
+                                    if (PARTS > 1) g[i] = bf16_part(g[i], part);
                                 }
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) w[i] = pack2(g[2 * i], g[2 * i + 1]);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    w[i] = pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                                for (int q = 0; q < 4; ++q)
+                                    st_shared_v4(piece + lane * 128 + (((hh * 4 + q) ^ (lane & 7)) << 4),
+                                                 pack2(g[8 * q], g[8 * q + 1]), pack2(g[8 * q + 2], g[8 * q + 3]),
+                                                 pack2(g[8 * q + 4], g[8 * q + 5]), pack2(g[8 * q + 6], g[8 * q + 7]));
                             }
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                st_shared_v4(piece + lane * 128 + (((hh * 4 + q) ^ (lane & 7)) << 4), w[4 * q],
-                                             w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0 && T.mt * BM + 32 * qd < p.m) {
-                            tma_store_3d(&tm_out, piece, (int)col0 + 64 * pc, (int)(T.mt * BM) + 32 * qd, part);
-                            bulk_commit();
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0 && some) {
+                                tma_store_3d(&tm_a2, piece, (int)col0 + 64 * pc, (int)(T.mt * BM + HM * rank) + 32 * qd,
+                                             part);
+                                bulk_commit();
+                            }
                         }
                     }
                 }
             }
-            tc_fence_before();
-            mbar_arrive(tempty0 + 8 * acc);
+            if (!SEG && T.kb0 < T.kb1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(lead_tempty + 8 * acc);
+                ++tc;
+            }
         }
         if (lane == 0) bulk_wait0();
     }
 
+    __syncwarp();
+    if (*abort_flag) {           // the other CTA's copies into this one end in microseconds; give them a millisecond
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000) {}
+    }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();              // no CTA leaves while the other one's MMAs or arrivals need it
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, TMEM_COLS);
+        pair_tmem_dealloc(tmem_base, TMEM_COLS);
     }
 }
 
 // ------------------------------------------------------------ small kernels
-// Joins the half tiles' (maximum, sum) of 32 rows: 8 warps take a strided
-// eighth of the tiles each (lane = row), then the eight are joined in order.
+// The sum of a product's slots, in order, as its rows of the output: a warp
+// for 32 rows x 32 columns.
+template <typename T>
+__global__ void __launch_bounds__(256) join_kernel(const Prod q, const int32_t* live, int d, int vec) {
+    __shared__ __align__(16) unsigned char stage[8][PIECE];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t rows = live ? *live : q.rows, cb = cdiv(d, 32), total = cdiv(rows, 32) * cb;
+    for (int64_t u = (int64_t)blockIdx.x * 8 + warp; u < total; u += (int64_t)gridDim.x * 8) {
+        const int64_t rb = u / cb, col = (u - rb * cb) * 32, row = rb * 32 + lane;
+        float v[32], f = 1.f;
+        int64_t to = -1;
+        if (row < rows) {
+            to = q.row_of ? q.row_of[row] : q.row0 + row;
+            f = q.scale ? *q.scale : 1.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        for (int s = 0; s < q.slots; ++s) {
+            const float* at = partial_at(q, d, s, rb, col) + lane;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += at[i * 32];
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= f;
+        emit(reinterpret_cast<T*>(q.out), d, vec != 0, to, col, v, smem_u32(stage[warp]), lane);
+    }
+}
+
+// Joins the half tiles' (maximum, sum) of 32 rows: 32 warps take a strided
+// part of the tiles each (lane = row), then theirs are joined in order.  The
+// last block to finish (a ticket) adds up all blocks' losses, in block order.
 __device__ __forceinline__ void lse_join(float& m, float& s, float m2, float s2) {
     if (s2 == 0.f) return;                        // nothing but -inf
     const float mx = fmaxf(m, m2);
     s = s * (m == mx ? 1.f : ex2((m - mx) * kLog2e)) + s2 * (m2 == mx ? 1.f : ex2((m2 - mx) * kLog2e));
     m = mx;
 }
-__global__ void __launch_bounds__(256) logsumexp_kernel(const float2* partials, int n_part, int64_t rows, int64_t row0,
-                                                        const float* zt, const int32_t* targets, int64_t vocab,
-                                                        float* loss, float* lse, float2* sums, void* ws) {
-    __shared__ float2 sh[8][32];
+__global__ void __launch_bounds__(1024) logsumexp_kernel(const float2* partials, int n_part, int64_t rows, int64_t row0,
+                                                         const float* zt, const int32_t* targets, int64_t vocab,
+                                                         float* loss, float* lse, float2* sums, int32_t* ticket,
+                                                         int64_t blocks, float* mean, void* ws) {
+    __shared__ float2 sh[32][33];
+    __shared__ double sl[32], sn[32];
+    __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = (int64_t)blockIdx.x * 32 + lane;
     float m = -INFINITY, s = 0.f;
     if (row < rows) {
-#pragma unroll 4
-        for (int q = warp; q < n_part; q += 8) {
-            const float2 v = partials[(int64_t)q * rows + row];
-            lse_join(m, s, v.x, v.y);
+        for (int q = warp; q < n_part; q += 32 * 4) {
+            float2 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                v[u] = q + 32 * u < n_part ? partials[(int64_t)(q + 32 * u) * rows + row] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) lse_join(m, s, v[u].x, v[u].y);
         }
     }
     sh[warp][lane] = make_float2(m, s);
     __syncthreads();
-    if (warp != 0) return;
+    // warp w joins row w's 32 parts, a fixed tree
+    {
+        const float2 v = sh[lane][warp];
+        m = v.x;
+        s = v.y;
 #pragma unroll
-    for (int w = 1; w < 8; ++w) lse_join(m, s, sh[w][lane].x, sh[w][lane].y);
-    float l = 0.f, n = 0.f;
-    if (row < rows) {
-        const float ls = m + log2f(s) * kLn2;
-        const int64_t tg = targets[row];
-        if (tg >= vocab) record_error(ws, MOM_DEVERR_TARGET, row0 + row);
-        if (tg >= 0 && tg < vocab) {
-            l = ls - zt[row];
-            n = 1.f;
+        for (int o = 1; o < 32; o <<= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+            float ma = (lane & o) ? m2 : m, sa = (lane & o) ? s2 : s;      // lower lane's part first, on both sides
+            lse_join(ma, sa, (lane & o) ? m : m2, (lane & o) ? s : s2);
+            m = ma;
+            s = sa;
         }
-        lse[row] = ls;
-        loss[row] = l;
     }
-    l = warp_sum(l);
-    n = warp_sum(n);
-    if (lane == 0) sums[row0 / 32 + blockIdx.x] = make_float2(l, n);
-}
-// mean[0] = sum of losses / rows counted, mean[1] = 1 / rows counted
-__global__ void __launch_bounds__(1024) mean_loss_kernel(const float2* sums, int64_t n, float* mean) {
-    __shared__ double sl[32], sn[32];
+    __syncthreads();
+    if (lane == 0) sh[0][warp] = make_float2(m, s);
+    __syncthreads();
+    if (warp == 0) {
+        m = sh[0][lane].x;
+        s = sh[0][lane].y;
+        float l = 0.f, n = 0.f;
+        if (row < rows) {
+            const float ls = m + log2f(s) * kLn2;
+            const int64_t tg = targets[row];
+            if (tg >= vocab) record_error(ws, MOM_DEVERR_TARGET, row0 + row);
+            if (tg >= 0 && tg < vocab) {
+                l = ls - zt[row];
+                n = 1.f;
+            }
+            lse[row] = ls;
+            loss[row] = l;
+        }
+        l = warp_sum(l);
+        n = warp_sum(n);
+        if (lane == 0) {
+            sums[row0 / 32 + blockIdx.x] = make_float2(l, n);
+            __threadfence();
+            last = mean && atomicAdd(ticket, 1) == blocks - 1;
+        }
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    // mean[0] = sum of losses / rows counted, mean[1] = 1 / rows counted
     double l = 0.0, c = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += 1024) {
-        const float2 v = sums[i];
+    for (int64_t i = threadIdx.x; i < blocks; i += 1024) {
+        const float2 v = __ldcg(sums + i);
         l += v.x;
         c += v.y;
     }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -445,38 +765,120 @@ __global__ void __launch_bounds__(1024) mean_loss_kernel(const float2* sums, int
     }
 }
 
+// A row of d elements as its bf16 parts (each `part` elements after
+// the one before) by one warp.  `vec`: both rows take 16-byte accesses.
+template <typename T, int PARTS>
+__device__ __forceinline__ void copy_row(const T* src, int d, bf16* dst, int64_t part, bool vec, int lane) {
+    if (PARTS == 1 && vec) {
+        for (int c = lane * 8; c < d; c += 256) {
+            float v[8];
+            load_vec<8>(src + c, v);
+            store_vec<8>(dst + c, v);
+        }
+        return;
+    }
+    for (int c = lane * 2; c < d; c += 64) {       // (pairs stay inside the pitch, which is even)
+        float v[2] = {to_f(src[c]), c + 1 < d ? to_f(src[c + 1]) : 0.f};
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[0], v[1]);
+            *reinterpret_cast<__nv_bfloat162*>(dst + q * part + c) = b;
+            v[0] -= __bfloat162float(b.x);
+            v[1] -= __bfloat162float(b.y);
+        }
+    }
+}
+
 // [rows, d] -> bf16 parts [parts][rows, pitch]: rows that TMA can stride over
 // (a pitch that is a multiple of 8), float32 split into its three parts.
 template <typename T, int PARTS>
 __global__ void __launch_bounds__(256) parts_kernel(const T* src, int64_t rows, int d, int pitch, bf16* dst) {
-    const int64_t n = rows * (int64_t)d, step = (int64_t)gridDim.x * 256, part = rows * (int64_t)pitch;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-        const int64_t r = i / d;
-        bf16* o = dst + r * pitch + (i - r * d);
-        if constexpr (PARTS == 1) {
-            *o = src[i];
-        } else {
-            float v = to_f(src[i]);
+    const int64_t step = (int64_t)gridDim.x * 8;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += step)
+        copy_row<T, PARTS>(src + r * d, d, dst + r * pitch, rows * pitch, false, threadIdx.x & 31);
+}
+
+// The rows that have a target, packed in order.  A block takes 64 rows; it
+// counts the targets before them itself (kCountRows at most; where there are
+// more, count_kernel has counted whole chunks of kCountRows).
+constexpr int kGatherRows = 64, kCountRows = 32768;
+struct GatherArgs {
+    const void* x;
+    const int32_t* targets;
+    const float *lse, *dloss;
+    const int32_t* counts;               // null: n <= kCountRows
+    int64_t n, vocab;
+    int d, pitch;
+    int64_t part;                        // elements between the parts
+    bf16* xc;                            // the packed rows
+    int32_t *targets_c, *row_of, *live;
+    float *lse2, *weight;                // log2(e) lse, dloss
+    void* dx;
+    int vec;                             // x, xc and dx take 16-byte accesses
+};
+__device__ __forceinline__ bool has_target(int32_t t, int64_t vocab) { return t >= 0 && t < vocab; }
+__device__ __forceinline__ int block_sum(int v) {
+    __shared__ int sh[8];
+    v = __reduce_add_sync(0xffffffffu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int s = 0;
 #pragma unroll
-            for (int q = 0; q < PARTS; ++q) {
-                const bf16 b = __float2bfloat16_rn(v);
-                o[q * part] = b;
-                v -= __bfloat162float(b);
-            }
+    for (int w = 0; w < 8; ++w) s += sh[w];
+    return s;
+}
+__global__ void __launch_bounds__(256) count_kernel(const int32_t* targets, int64_t n, int64_t vocab, int32_t* counts) {
+    const int64_t r0 = (int64_t)blockIdx.x * kCountRows, r1 = r0 + kCountRows < n ? r0 + kCountRows : n;
+    int v = 0;
+    for (int64_t r = r0 + threadIdx.x; r < r1; r += 256) v += has_target(targets[r], vocab);
+    v = block_sum(v);
+    if (threadIdx.x == 0) counts[blockIdx.x] = v;
+}
+template <typename T, int PARTS>
+__global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
+    __shared__ int place[kGatherRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t r0 = (int64_t)blockIdx.x * kGatherRows, chunk = r0 / kCountRows;
+    int before = 0;
+    for (int64_t i = threadIdx.x; i < chunk; i += 256) before += a.counts[i];
+#pragma unroll 4
+    for (int64_t r = chunk * kCountRows + threadIdx.x; r < r0; r += 256) before += has_target(a.targets[r], a.vocab);
+    before = block_sum(before);
+    int live = before;
+#pragma unroll
+    for (int h = 0; h < kGatherRows; h += 32) {
+        const bool in = r0 + h + lane < a.n && has_target(a.targets[r0 + h + lane], a.vocab);
+        const uint32_t m = __ballot_sync(0xffffffffu, in);
+        if (warp == 0) place[h + lane] = in ? live + __popc(m & ((1u << lane) - 1)) : -1;
+        live += __popc(m);
+    }
+    __syncthreads();
+    for (int i = warp; i < kGatherRows && r0 + i < a.n; i += 8) {
+        const int64_t row = r0 + i, to = place[i];
+        if (to < 0) {                              // dx of padding is 0
+            T* o = reinterpret_cast<T*>(a.dx) + row * a.d;
+            const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (a.vec) for (int c = lane * 8; c < a.d; c += 256) store_vec<8>(o + c, z);
+            else for (int c = lane; c < a.d; c += 32) o[c] = from_f<T>(0.f);
+            continue;
+        }
+        const T* x = reinterpret_cast<const T*>(a.x) + row * a.d;
+        copy_row<T, PARTS>(x, a.d, a.xc + to * a.pitch, a.part, a.vec != 0, lane);
+        if (lane == 0) {
+            a.targets_c[to] = a.targets[row];
+            a.row_of[to] = (int32_t)row;
+            a.lse2[to] = a.lse[row] * kLog2e;
+            if (a.dloss) a.weight[to] = a.dloss[row];
         }
     }
-}
-// out [rows, d] = sum over slots of in [slots][rows, pitch], in slot order
-template <typename TI, typename TO>
-__global__ void __launch_bounds__(256) join_kernel(const TI* in, int slots, int64_t rows, int d, int pitch, TO* out) {
-    const int64_t n = rows * (int64_t)d, step = (int64_t)gridDim.x * 256, slot = rows * (int64_t)pitch;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-        const int64_t r = i / d;
-        const TI* p = in + r * pitch + (i - r * d);
-        float v = to_f(*p);
-        for (int s = 1; s < slots; ++s) v += to_f(p[s * slot]);
-        out[i] = from_f<TO>(v);
-    }
+    if (r0 + kGatherRows < a.n) return;
+    // the last block: the number of rows, and zeros up to whole K blocks of dW
+    if (threadIdx.x == 0) *a.live = live;
+    for (int64_t r = live + warp; r < cdiv(live, BK) * BK; r += 8)
+        for (int q = 0; q < PARTS; ++q)
+            for (int c = lane * 2; c < a.d; c += 64)
+                *reinterpret_cast<__nv_bfloat162*>(a.xc + q * a.part + r * a.pitch + c) = __floats2bfloat162_rn(0.f, 0.f);
 }
 
 // ------------------------------------------------------------------- host
@@ -495,93 +897,86 @@ constexpr int64_t kPieceBytes = 512LL << 20;     // of g, and of a split or padd
 
 struct Plan {
     int parts;             // bf16 parts of an operand
-    bool direct;           // x, w, dx, dw are read and written in place by TMA
-    int pitch;             // row pitch of copied operands and staged outputs (elements)
+    bool direct;           // x (forward) and w are read in place by TMA
+    int pitch;             // row pitch of copied operands (elements)
     int64_t piece;         // classes of a piece (a multiple of 256)
+    int64_t xrows;         // rows of the packed x
+    int bn;                // columns of an OUT tile
     int sx, sw;            // K slots of dx and dw
-    bool dx_direct, dw_direct;
-    size_t zt, partials, sums, xbuf, wbuf, g, dxs, dws, bytes;
+    bool dx_partial, dw_partial;
+    size_t zt, partials, sums, ticket, xbuf, wbuf, g, dxp, dwp, targets, row_of, lse2, weight, live, counts, bytes;
 };
-
-int slots_for(int64_t tiles, int64_t kb, int sms) {
-    if (2 * tiles > sms) return 1;
-    int64_t s = sms / tiles;
-    if (s > kb / 8) s = kb / 8;                  // at least 512 of K a slot
-    if (s < 1) s = 1;
-    const int64_t per = cdiv(kb, s);
-    return (int)cdiv(kb, per);
-}
 
 Plan plan_for(int64_t n, int d, int64_t v, int dt, bool bwd) {
     Plan L{};
-    const int sms = sm_count();
+    const int clusters = sm_count() / 2;
     const bool b16 = dt == MOM_BF16;
     L.parts = b16 ? 1 : 3;
     L.direct = b16 && d % 8 == 0;
     L.pitch = (int)up(d, 8);
+    L.xrows = bwd ? up(n, BK) : n;
     int64_t piece = kPieceBytes / (2 * L.parts * (n > L.pitch ? n : L.pitch)) / 256 * 256;
     if (piece < 256) piece = 256;
     const int64_t np = cdiv(v, piece);
     L.piece = up(cdiv(v, np), 256);
     size_t o = MOM_WS_HEADER_BYTES;
     auto take = [&](size_t b) { const size_t at = o; o += up256(b); return at; };
-    if (!L.direct) {
-        L.xbuf = take((size_t)L.parts * n * L.pitch * 2);
-        L.wbuf = take((size_t)L.parts * L.piece * L.pitch * 2);
-    }
+    if (!L.direct) L.wbuf = take((size_t)L.parts * L.piece * L.pitch * 2);
+    if (!L.direct || bwd) L.xbuf = take((size_t)L.parts * L.xrows * L.pitch * 2);
     if (!bwd) {
         const int64_t rows = n < kRowChunk ? n : kRowChunk;
         L.zt = take(rows * 4);
         L.partials = take((size_t)rows * 2 * cdiv(v, BN) * 8);
         L.sums = take((size_t)cdiv(n, 32) * 8);
+        L.ticket = take(4);
     } else {
-        const int64_t kb = cdiv(v < L.piece ? v : L.piece, BK), tiles = cdiv(n, BM) * cdiv(d, BN);
-        L.sx = slots_for(tiles, kb, sms);
-        L.sw = slots_for(cdiv(L.piece, BM) * cdiv(d, BN), cdiv(n, BK), sms);
-        L.dx_direct = L.sx == 1 && L.piece >= v && (b16 ? d % 8 == 0 : d % 4 == 0);
-        L.dw_direct = L.sw == 1 && (b16 ? d % 8 == 0 : d % 4 == 0);
-        L.g = take((size_t)L.parts * n * L.piece * 2);
-        if (!L.dx_direct) L.dxs = take((size_t)L.sx * n * L.pitch * 4);
-        if (!L.dw_direct) L.dws = take((size_t)L.sw * L.piece * L.pitch * 4);
+        L.bn = d <= 128 ? 128 : BN;
+        // K blocks of a tile, and of a cluster's share of a piece with each
+        // tile's epilogue counted as 4 of them
+        const int64_t nt = cdiv(d, L.bn), k1 = cdiv(v < L.piece ? v : L.piece, BK), k2 = cdiv(n, BK);
+        const int64_t t1 = cdiv(n, BM) * nt, t2 = cdiv(L.piece, BM) * nt;
+        int64_t share = cdiv(t1 * (k1 + 4) + t2 * (k2 + 4), clusters);
+        if (share < 16) share = 16;
+        L.sx = (int)cdiv(k1, share);
+        L.sw = (int)cdiv(k2, share);
+        L.dx_partial = L.sx > 1 || L.piece < v;
+        L.dw_partial = L.sw > 1;
+        L.g = take((size_t)L.parts * L.xrows * L.piece * 2);
+        if (L.dx_partial) L.dxp = take((size_t)L.sx * up(n, 32) * up(d, 32) * 4);
+        if (L.dw_partial) L.dwp = take((size_t)L.sw * up(L.piece, 32) * up(d, 32) * 4);
+        L.targets = take(n * 4);
+        L.row_of = take(n * 4);
+        L.lse2 = take(n * 4);
+        L.weight = take(n * 4);
+        L.live = take(4);
+        L.counts = take(cdiv(n, kCountRows) * 4);
     }
     L.bytes = o;
     return L;
 }
 
-template <int EPI, bool A_MN, bool B_MN>
-cudaError_t run_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, GemmArgs p, int splits,
-                     int parts, cudaStream_t st) {
-    p.m_tiles = cdiv(p.m, BM);
-    p.n_tiles = cdiv(p.n, BN);
-    p.kb_split = (int)cdiv(p.kb_total, splits);
-    p.tiles = p.m_tiles * p.n_tiles * splits;
-    if (parts == 1) {
-        p.n_pairs = 1;
-        p.pa[0] = p.pb[0] = 0;
-    } else {
-        static const uint8_t A6[6] = {2, 1, 0, 1, 0, 0}, B6[6] = {0, 1, 2, 0, 1, 0};
-        p.n_pairs = 6;
-        for (int i = 0; i < 6; ++i) { p.pa[i] = A6[i]; p.pb[i] = B6[i]; }
-    }
+template <int PARTS, int EPI>
+cudaError_t run_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2, const CUtensorMap& b2,
+                     const GemmArgs& p, int64_t tiles, cudaStream_t st) {
     static unsigned long long optin_done = 0;
-    auto* k = ce_gemm_kernel<EPI, A_MN, B_MN>;
-    cudaError_t e = smem_optin((const void*)k, (int)SMEM_BYTES, &optin_done);
+    auto* k = ce_gemm_kernel<PARTS, EPI>;
+    const cudaError_t e = smem_optin((const void*)k, (int)smem_bytes<PARTS>(), &optin_done);
     if (e != cudaSuccess) return e;
-    const int sms = sm_count();
-    k<<<(unsigned)(p.tiles < sms ? p.tiles : sms), THREADS, SMEM_BYTES, st>>>(a, b, out, p);
+    const int64_t clusters = sm_count() / 2;
+    k<<<(unsigned)(2 * (tiles < clusters ? tiles : clusters)), THREADS, smem_bytes<PARTS>(), st>>>(a, b, a2, b2, p);
     count_launches(1);
     return cudaGetLastError();
 }
 
-unsigned ew_grid(int64_t n) {
-    const int64_t b = cdiv(n, 256), most = (int64_t)sm_count() * 16;
+unsigned warps_grid(int64_t warps) {
+    const int64_t b = cdiv(warps, 8), most = (int64_t)sm_count() * 16;
     return (unsigned)(b < most ? b : most);
 }
 
 cudaError_t to_parts(const void* src, int dt, int64_t rows, int d, int pitch, void* dst, cudaStream_t st) {
     bf16* o = reinterpret_cast<bf16*>(dst);
-    if (dt == MOM_BF16) parts_kernel<bf16, 1><<<ew_grid(rows * d), 256, 0, st>>>(reinterpret_cast<const bf16*>(src), rows, d, pitch, o);
-    else parts_kernel<float, 3><<<ew_grid(rows * d), 256, 0, st>>>(reinterpret_cast<const float*>(src), rows, d, pitch, o);
+    if (dt == MOM_BF16) parts_kernel<bf16, 1><<<warps_grid(rows), 256, 0, st>>>(reinterpret_cast<const bf16*>(src), rows, d, pitch, o);
+    else parts_kernel<float, 3><<<warps_grid(rows), 256, 0, st>>>(reinterpret_cast<const float*>(src), rows, d, pitch, o);
     count_launches(1);
     return cudaGetLastError();
 }
@@ -606,13 +1001,7 @@ cudaError_t w_piece(const LinearCeArgs& a, const Plan& L, int64_t v0, int64_t pw
 #define MOM_TRY(x) do { const cudaError_t e_ = (x); if (e_ != cudaSuccess) return e_; } while (0)
 #define MOM_MAP(x) do { if (!(x)) return cudaErrorInvalidValue; } while (0)
 
-}  // namespace
-
-size_t linear_ce_workspace_bytes(int64_t n, int d, int64_t v, int dt, bool bwd) {
-    return plan_for(n > 0 ? n : 1, d, v, dt, bwd).bytes;
-}
-
-cudaError_t launch_linear_ce_fwd(const LinearCeArgs& a, cudaStream_t st) {
+template <int PARTS> cudaError_t fwd(const LinearCeArgs& a, cudaStream_t st) {
     const Plan L = plan_for(a.n, a.d, a.v, a.dt, false);
     char* ws = reinterpret_cast<char*>(a.ws);
     if (!L.direct) MOM_TRY(to_parts(a.x, a.dt, a.n, a.d, L.pitch, ws + L.xbuf, st));
@@ -620,129 +1009,154 @@ cudaError_t launch_linear_ce_fwd(const LinearCeArgs& a, cudaStream_t st) {
     const int n_part = (int)(2 * cdiv(a.v, BN));
     float2* partials = reinterpret_cast<float2*>(ws + L.partials);
     float* zt = reinterpret_cast<float*>(ws + L.zt);
+    int32_t* ticket = reinterpret_cast<int32_t*>(ws + L.ticket);
     for (int64_t r0 = 0; r0 < a.n; r0 += kRowChunk) {
         const int64_t rows = a.n - r0 < kRowChunk ? a.n - r0 : kRowChunk;
         CUtensorMap ma, mb;
         // the chunk's rows: a map that starts at r0; the parts lie n rows apart
-        MOM_MAP(make_tma_3d(&ma, reinterpret_cast<const bf16*>(xb) + r0 * L.pitch, false, a.d, rows, L.parts, L.pitch,
-                            BM, a.n));
+        MOM_MAP(make_tma_3d(&ma, reinterpret_cast<const bf16*>(xb) + r0 * L.pitch, false, a.d, rows, PARTS, L.pitch,
+                            HM, a.n));
         for (int64_t v0 = 0; v0 < a.v; v0 += L.direct ? a.v : L.piece) {
             const int64_t pw = L.direct ? a.v : a.v - v0 < L.piece ? a.v - v0 : L.piece;
             WPiece w;
             MOM_TRY(w_piece(a, L, v0, pw, w, st));
-            MOM_MAP(make_tma_3d(&mb, w.base, false, a.d, w.rows, L.parts, w.pitch, BN));
+            MOM_MAP(make_tma_3d(&mb, w.base, false, a.d, w.rows, PARTS, w.pitch, HM));
             GemmArgs p{};
-            p.m = rows;
-            p.n = pw;
-            p.kb_total = (int)cdiv(a.d, BK);
+            p.rows = rows;
+            p.cols = pw;
+            p.kb = (int)cdiv(a.d, BK);
             p.b_row0 = w.row0;
             p.targets = a.targets + r0;
             p.v0 = v0;
             p.vocab = a.v;
             p.partials = partials + v0 / BN * 2 * rows;
             p.zt = zt;
+            p.ticket = r0 == 0 ? ticket : nullptr;
             p.ws = a.ws;
-            MOM_TRY((run_gemm<EPI_STATS, false, false>(ma, mb, ma, p, 1, L.parts, st)));
+            MOM_TRY((run_gemm<PARTS, EPI_STATS>(ma, mb, ma, mb, p, cdiv(rows, BM) * cdiv(pw, BN), st)));
         }
-        logsumexp_kernel<<<(unsigned)cdiv(rows, 32), 256, 0, st>>>(partials, n_part, rows, r0, zt, a.targets + r0, a.v,
-                                                                   a.loss + r0, a.lse + r0,
-                                                                   reinterpret_cast<float2*>(ws + L.sums), a.ws);
+        logsumexp_kernel<<<(unsigned)cdiv(rows, 32), 1024, 0, st>>>(
+            partials, n_part, rows, r0, zt, a.targets + r0, a.v, a.loss + r0, a.lse + r0,
+            reinterpret_cast<float2*>(ws + L.sums), ticket, cdiv(a.n, 32), a.mean, a.ws);
         count_launches(1);
         MOM_TRY(cudaGetLastError());
     }
-    if (a.mean) {
-        mean_loss_kernel<<<1, 1024, 0, st>>>(reinterpret_cast<const float2*>(ws + L.sums), cdiv(a.n, 32), a.mean);
-        count_launches(1);
-    }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
-cudaError_t launch_linear_ce_bwd(const LinearCeArgs& a, cudaStream_t st) {
+template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
+    typedef typename std::conditional<PARTS == 1, bf16, float>::type T;
     const Plan L = plan_for(a.n, a.d, a.v, a.dt, true);
-    const bool b16 = a.dt == MOM_BF16;
-    const size_t es = b16 ? 2 : 4;
     char* ws = reinterpret_cast<char*>(a.ws);
-    if (!L.direct) MOM_TRY(to_parts(a.x, a.dt, a.n, a.d, L.pitch, ws + L.xbuf, st));
-    const void* xb = L.direct ? a.x : ws + L.xbuf;
+    auto i32 = [&](size_t at) { return reinterpret_cast<int32_t*>(ws + at); };
+    auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    const bool vec = a.d % (16 / (int)sizeof(T)) == 0;         // of dx's and dw's rows
+    bf16* xc = reinterpret_cast<bf16*>(ws + L.xbuf);
+    const int32_t* live = i32(L.live);
+    {
+        GatherArgs g{};
+        g.x = a.x;
+        g.targets = a.targets;
+        g.lse = a.lse;
+        g.dloss = a.dloss;
+        g.counts = i32(L.counts);
+        g.n = a.n;
+        g.vocab = a.v;
+        g.d = a.d;
+        g.pitch = L.pitch;
+        g.part = L.xrows * L.pitch;
+        g.xc = xc;
+        g.targets_c = i32(L.targets);
+        g.row_of = i32(L.row_of);
+        g.live = i32(L.live);
+        g.lse2 = f32(L.lse2);
+        g.weight = f32(L.weight);
+        g.dx = a.dx;
+        g.vec = a.d % 8 == 0;
+        if (a.n > kCountRows) {
+            count_kernel<<<(unsigned)cdiv(a.n, kCountRows), 256, 0, st>>>(a.targets, a.n, a.v, i32(L.counts));
+            count_launches(1);
+            MOM_TRY(cudaGetLastError());
+        }
+        gather_kernel<T, PARTS><<<(unsigned)cdiv(a.n, kGatherRows), 256, 0, st>>>(g);
+        count_launches(1);
+        MOM_TRY(cudaGetLastError());
+    }
     CUtensorMap mx_k, mx_mn;       // x: K-major rows of the logits; MN-major rows (K = tokens) of dw
-    MOM_MAP(make_tma_3d(&mx_k, xb, false, a.d, a.n, L.parts, L.pitch, BM));
-    MOM_MAP(make_tma_3d(&mx_mn, xb, false, a.d, a.n, L.parts, L.pitch, BK));
+    MOM_MAP(make_tma_3d(&mx_k, xc, false, a.d, L.xrows, PARTS, L.pitch, HM));
+    MOM_MAP(make_tma_3d(&mx_mn, xc, false, a.d, L.xrows, PARTS, L.pitch, BK));
+    const int64_t mt = cdiv(a.n, BM);
     for (int64_t v0 = 0; v0 < a.v; v0 += L.piece) {
         const int64_t pw = a.v - v0 < L.piece ? a.v - v0 : L.piece;
         WPiece w;
         MOM_TRY(w_piece(a, L, v0, pw, w, st));
-        CUtensorMap mw_k, mw_mn, mg_st, mg_k, mg_mn, mo;
-        MOM_MAP(make_tma_3d(&mw_k, w.base, false, a.d, w.rows, L.parts, w.pitch, BN));
-        MOM_MAP(make_tma_3d(&mw_mn, w.base, false, a.d, w.rows, L.parts, w.pitch, BK));
-        MOM_MAP(make_tma_3d(&mg_st, ws + L.g, false, L.piece, a.n, L.parts, L.piece, 32));
-        MOM_MAP(make_tma_3d(&mg_k, ws + L.g, false, L.piece, a.n, L.parts, L.piece, BM));
-        MOM_MAP(make_tma_3d(&mg_mn, ws + L.g, false, L.piece, a.n, L.parts, L.piece, BK));
-        {   // g of the piece
-            GemmArgs p{};
-            p.m = a.n;
-            p.n = pw;
-            p.kb_total = (int)cdiv(a.d, BK);
-            p.b_row0 = w.row0;
-            p.targets = a.targets;
-            p.v0 = v0;
-            p.vocab = a.v;
-            p.lse = a.lse;
-            p.dloss = a.dloss;
-            p.dscale = a.dscale;
-            p.n_parts = L.parts;
-            p.ws = a.ws;
-            MOM_TRY((run_gemm<EPI_GRAD, false, false>(mx_k, mw_k, mg_st, p, 1, L.parts, st)));
+        CUtensorMap mw_k, mw_mn, mg_st, mg_k, mg_mn;
+        MOM_MAP(make_tma_3d(&mw_k, w.base, false, a.d, w.rows, PARTS, w.pitch, HM));
+        MOM_MAP(make_tma_3d(&mw_mn, w.base, false, a.d, w.rows, PARTS, w.pitch, BK));
+        MOM_MAP(make_tma_3d(&mg_st, ws + L.g, false, L.piece, L.xrows, PARTS, L.piece, 32));
+        MOM_MAP(make_tma_3d(&mg_k, ws + L.g, false, L.piece, L.xrows, PARTS, L.piece, HM));
+        MOM_MAP(make_tma_3d(&mg_mn, ws + L.g, false, L.piece, L.xrows, PARTS, L.piece, BK));
+        GemmArgs p{};
+        p.rows = a.n;
+        p.cols = pw;
+        p.kb = (int)cdiv(a.d, BK);
+        p.b_row0 = w.row0;
+        p.live = live;
+        p.targets = i32(L.targets);
+        p.v0 = v0;
+        p.vocab = a.v;
+        p.lse2 = f32(L.lse2);
+        p.weight = a.dloss ? f32(L.weight) : nullptr;
+        p.ws = a.ws;
+        MOM_TRY((run_gemm<PARTS, EPI_GRAD>(mx_k, mw_k, mg_st, mw_k, p, mt * cdiv(pw, BN), st)));
+        p.d = a.d;
+        p.bn = L.bn;
+        p.vec = vec;
+        p.dx.rows = a.n;
+        p.dx.kb = (int)cdiv(pw, BK);
+        p.dx.slots = L.sx;
+        p.dx.out = a.dx;
+        p.dx.row_of = i32(L.row_of);
+        p.dx.scale = a.dscale;
+        p.dx.partial = L.dx_partial ? f32(L.dxp) : nullptr;
+        p.dx.add = v0 > 0;
+        p.dx.last = v0 + L.piece >= a.v;
+        p.dw.rows = pw;
+        p.dw.row0 = v0;
+        p.dw.kb = (int)cdiv(a.n, BK);
+        p.dw.slots = L.sw;
+        p.dw.out = a.dw;
+        p.dw.scale = a.dscale;
+        p.dw.partial = L.dw_partial ? f32(L.dwp) : nullptr;
+        p.dw.last = 1;
+        const int64_t nt = cdiv(a.d, L.bn), tiles = mt * nt * L.sx + cdiv(pw, BM) * nt * L.sw;
+        MOM_TRY((run_gemm<PARTS, EPI_OUT>(mg_k, mw_mn, mg_mn, mx_mn, p, tiles, st)));
+        if (L.sx > 1 && p.dx.last) {
+            join_kernel<T><<<warps_grid(cdiv(a.n, 32) * cdiv(a.d, 32)), 256, 0, st>>>(p.dx, live, a.d, vec);
+            count_launches(1);
+            MOM_TRY(cudaGetLastError());
         }
-        {   // dx (+)= g W
-            GemmArgs p{};
-            p.m = a.n;
-            p.n = a.d;
-            p.kb_total = (int)cdiv(pw, BK);
-            p.b_row0 = w.row0;
-            p.add = v0 > 0;
-            p.ws = a.ws;
-            const int64_t per = cdiv(p.kb_total, L.sx);
-            const int splits = (int)cdiv(p.kb_total, per);       // a short last piece may fill fewer slots
-            if (L.dx_direct && b16) {
-                MOM_MAP(make_tma_3d(&mo, a.dx, false, a.d, a.n, 1, a.d, 32));
-                MOM_TRY((run_gemm<EPI_BF16, false, true>(mg_k, mw_mn, mo, p, 1, L.parts, st)));
-            } else {
-                void* out = L.dx_direct ? a.dx : ws + L.dxs;
-                MOM_MAP(make_tma_3d(&mo, out, true, a.d, a.n, L.sx, L.dx_direct ? a.d : L.pitch, 32));
-                MOM_TRY((run_gemm<EPI_F32, false, true>(mg_k, mw_mn, mo, p, splits, L.parts, st)));
-            }
-        }
-        {   // dw = g^T x
-            GemmArgs p{};
-            p.m = pw;
-            p.n = a.d;
-            p.kb_total = (int)cdiv(a.n, BK);
-            p.ws = a.ws;
-            char* dw = reinterpret_cast<char*>(a.dw) + (size_t)v0 * a.d * es;
-            if (L.dw_direct && b16) {
-                MOM_MAP(make_tma_3d(&mo, dw, false, a.d, pw, 1, a.d, 32));
-                MOM_TRY((run_gemm<EPI_BF16, true, true>(mg_mn, mx_mn, mo, p, 1, L.parts, st)));
-            } else {
-                void* out = L.dw_direct ? dw : ws + L.dws;
-                MOM_MAP(make_tma_3d(&mo, out, true, a.d, pw, L.sw, L.dw_direct ? a.d : L.pitch, 32));
-                MOM_TRY((run_gemm<EPI_F32, true, true>(mg_mn, mx_mn, mo, p, L.sw, L.parts, st)));
-                if (!L.dw_direct) {
-                    const float* in = reinterpret_cast<const float*>(ws + L.dws);
-                    if (b16) join_kernel<float, bf16><<<ew_grid(pw * a.d), 256, 0, st>>>(in, L.sw, pw, a.d, L.pitch, reinterpret_cast<bf16*>(dw));
-                    else join_kernel<float, float><<<ew_grid(pw * a.d), 256, 0, st>>>(in, L.sw, pw, a.d, L.pitch, reinterpret_cast<float*>(dw));
-                    count_launches(1);
-                    MOM_TRY(cudaGetLastError());
-                }
-            }
+        if (L.sw > 1) {
+            join_kernel<T><<<warps_grid(cdiv(pw, 32) * cdiv(a.d, 32)), 256, 0, st>>>(p.dw, nullptr, a.d, vec);
+            count_launches(1);
+            MOM_TRY(cudaGetLastError());
         }
     }
-    if (!L.dx_direct) {
-        const float* in = reinterpret_cast<const float*>(ws + L.dxs);
-        if (b16) join_kernel<float, bf16><<<ew_grid(a.n * a.d), 256, 0, st>>>(in, L.sx, a.n, a.d, L.pitch, reinterpret_cast<bf16*>(a.dx));
-        else join_kernel<float, float><<<ew_grid(a.n * a.d), 256, 0, st>>>(in, L.sx, a.n, a.d, L.pitch, reinterpret_cast<float*>(a.dx));
-        count_launches(1);
-    }
-    return cudaGetLastError();
+    return cudaSuccess;
+}
+
+}  // namespace
+
+size_t linear_ce_workspace_bytes(int64_t n, int d, int64_t v, int dt, bool bwd) {
+    return plan_for(n > 0 ? n : 1, d, v, dt, bwd).bytes;
+}
+
+cudaError_t launch_linear_ce_fwd(const LinearCeArgs& a, cudaStream_t st) {
+    return a.dt == MOM_BF16 ? fwd<1>(a, st) : fwd<3>(a, st);
+}
+
+cudaError_t launch_linear_ce_bwd(const LinearCeArgs& a, cudaStream_t st) {
+    return a.dt == MOM_BF16 ? bwd<1>(a, st) : bwd<3>(a, st);
 }
 
 }  // namespace mom

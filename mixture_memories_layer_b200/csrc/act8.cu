@@ -49,8 +49,10 @@ __global__ void __launch_bounds__(kThreads) act8_pack_kernel(const T* __restrict
         for (int k = 0; k < kUnroll; ++k) {
             if (u + k * step < total) {
                 float f[8];
+                uint32_t m[2];
                 r[k].get(f);
-                act8_store<VEC>(f, w[k].c0, FLAT ? kChunk : d, lane, codes + w[k].row * (FLAT ? kChunk : d),
+                r[k].amax(m);
+                act8_store<VEC>(f, m, w[k].c0, FLAT ? kChunk : d, lane, codes + w[k].row * (FLAT ? kChunk : d),
                                 scales + w[k].row * (FLAT ? 2 : groups));
             }
         }

@@ -38,328 +38,319 @@ template <bool VEC> struct RawX<Q8, VEC> {
     __device__ __forceinline__ void get(float* out) const { r.get(out); }
 };
 
-// sigma(z): the hardware exponential and reciprocal, below 2^-21 relative for
-// |z| < 8 (2^-18 at |z| = 60, where sigma or 1 - sigma is 1e-26); a correctly
-// rounded division cost 15 of the 50 instructions an element took.
-__device__ __forceinline__ float fast_sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// sigma(z) = 1 / (1 + e), e = exp(-z), by the hardware exponential and
+// reciprocal: below 2^-21 relative for |z| < 8 (2^-18 at |z| = 60, where sigma
+// or 1 - sigma is 1e-26).  1 - sigma without cancellation: e sigma for z > 0.
+__device__ __forceinline__ float sigmoid(float z, float& rest) {
+    const float e = fast_ex2(z * -1.4426950408889634f), s = fast_rcp(1.f + e);
+    rest = z > 0.f ? e * s : 1.f - s;
+    return s;
+}
+__device__ __forceinline__ float sigmoid(float z) { return fast_rcp(1.f + fast_ex2(z * -1.4426950408889634f)); }
 
-// Sums of K values over the W = blockDim / 32 warps of a row (every thread
-// gets them); one warp a row needs no barrier.  `buf` alternates so that one
-// barrier is enough.
-template <int K> __device__ __forceinline__ void row_sum(float (&v)[K], float* buf, int W, int warp, int lane) {
-    warp_sum_n<K>(v);
-    if (W > 1) {
-        if (lane == 0)
-#pragma unroll
-            for (int k = 0; k < K; ++k) buf[warp * K + k] = v[k];
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] = 0.f;
-        for (int w = 0; w < W; ++w)
-#pragma unroll
-            for (int k = 0; k < K; ++k) v[k] += buf[w * K + k];
+constexpr int kWarps = 8;        // warps of a row's CTA; wider rows take a cluster of CTAs
+constexpr int kMaxCluster = 8;
+static_assert(kMaxCluster * kWarps * kChunk >= MOM_NORM_MAX_D, "a cluster holds a row");
+
+// Who holds what of a row: W warps a CTA with one chunk of 256 channels each,
+// in `cl` CTAs.  One warp a row: every warp of the CTA has its own.
+struct Place {
+    int lane, W, warp, cl, rank, c0;
+    __device__ __forceinline__ Place(const ResNormArgs& a) {
+        lane = threadIdx.x & 31;
+        W = a.warps_per_row;
+        warp = W > 1 ? threadIdx.x >> 5 : 0;
+        cl = a.cluster;
+        asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+        c0 = (rank * W + warp) * kChunk;
     }
+};
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-constexpr int kMaxWarps = 16;
+// Sums of K values over a row (every thread gets them), in warp order.  One
+// warp a row needs no barrier; in a cluster each warp writes its sums to every
+// CTA's shared memory and one cluster barrier takes the place of the CTA's.
+template <int K> __device__ __forceinline__ void row_sum(float (&v)[K], float* buf, const Place& w) {
+    warp_sum_n<K>(v);
+    if (w.W * w.cl == 1) return;
+    if (w.cl > 1) {
+        if (w.lane < w.cl) {
+            uint32_t at;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;"
+                : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(buf)), "r"(w.lane));
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                asm volatile("st.shared::cluster.f32 [%0], %1;"
+                             ::"r"(at + 4 * ((w.rank * w.W + w.warp) * K + k)), "f"(v[k]) : "memory");
+        }
+        cluster_barrier();
+    } else {
+        if (w.lane == 0)
+#pragma unroll
+            for (int k = 0; k < K; ++k) buf[w.warp * K + k] = v[k];
+        __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = 0.f;
+    for (int i = 0; i < w.W * w.cl; ++i)
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] += buf[i * K + k];
+}
 
-// W > 1: a CTA of W warps holds one row.  W == 1: each warp holds its own.
-template <typename XT, typename T, bool VEC, int C, int MAXW>
-__global__ void __launch_bounds__(32 * MAXW) residual_norm_kernel(const ResNormArgs a) {
-    __shared__ float red[2][kMaxWarps];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    const int W = a.warps_per_row, warp = W > 1 ? wid : 0;
-    const int64_t row = W > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * nw + wid;
-    if (row >= a.n_rows) return;      // whole CTAs (W > 1) or whole warps (W == 1)
+// The column weights of a thread's channels, res_scale * w_post and w_pre, in
+// registers for all of a CTA's rows.
+template <bool VEC> struct Weights {
+    float post[8], pre[8];
+    __device__ __forceinline__ Weights(const ResNormArgs& a, bool has_pre, const Place& w) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) post[i] = pre[i] = 0.f;
+        if (a.y) load8<VEC>(a.w_post, w.c0, a.d, w.lane, post);
+        if (a.y && a.res_scale) {
+            float s[8];
+            load8<VEC>(a.res_scale, w.c0, a.d, w.lane, s);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) post[i] *= s[i];
+        }
+        if (has_pre) load8<VEC>(a.w_pre, w.c0, a.d, w.lane, pre);
+    }
+};
+
+// A row's operands of the forward, as they lie in memory.
+template <typename XT, typename T, bool VEC> struct FwdRow {
+    RawX<XT, VEC> x;
+    Raw8<T, VEC> y, g;
+    T gate;
+    __device__ __forceinline__ void load(const ResNormArgs& a, int64_t row, const Place& w) {
+        if (row >= a.n_rows) return;
+        if (a.y) y.load(reinterpret_cast<const T*>(a.y) + row * a.d, w.c0, a.d, w.lane);
+        x.load(a, row, w.c0, w.lane);
+        if (a.gate_mode == MOM_GATE_ELEMENT) g.load(reinterpret_cast<const T*>(a.gate) + row * a.d, w.c0, a.d, w.lane);
+        if (a.gate_mode == MOM_GATE_TOKEN) gate = reinterpret_cast<const T*>(a.gate)[row];
+    }
+};
+
+// CTAs (clusters; warps, with one warp a row) walk the rows, the next one's
+// operands loaded before this one's arithmetic.  `red` alternates between two
+// rows, so that one barrier a sum is enough.
+template <typename XT, typename T, bool VEC>
+__global__ void __launch_bounds__(32 * kWarps, 2) residual_norm_kernel(const ResNormArgs a) {
+    __shared__ float red[2][2][kMaxCluster * kWarps];
+    const Place w(a);
+    const int rows_cta = w.W > 1 ? 1 : blockDim.x >> 5;
+    const int64_t step = (int64_t)gridDim.x / w.cl * rows_cta;
+    int64_t row = (int64_t)(blockIdx.x / w.cl) * rows_cta + (w.W > 1 ? 0 : threadIdx.x >> 5);
     const int d = a.d;
     const float inv_d = 1.f / (float)d;
-    RawX<XT, VEC> xr[C];
-    float xv[C][8];
-    if (a.y) {
-        Raw8<T, VEC> yr[C], gr[C];
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-            yr[j].load(reinterpret_cast<const T*>(a.y) + row * d, (warp + j * W) * kChunk, d, lane);
-#pragma unroll
-        for (int j = 0; j < C; ++j) xr[j].load(a, row, (warp + j * W) * kChunk, lane);
-        if (a.gate_mode == MOM_GATE_ELEMENT) {
-#pragma unroll
-            for (int j = 0; j < C; ++j)
-                gr[j].load(reinterpret_cast<const T*>(a.gate) + row * d, (warp + j * W) * kChunk, d, lane);
-        }
-        float gt = 1.f;
-        if (a.gate_mode == MOM_GATE_TOKEN) gt = fast_sigmoid(to_f(reinterpret_cast<const T*>(a.gate)[row]));
-        float ss[1] = {0.f};
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            float y[8];
-            yr[j].get(y);
+    FwdRow<XT, T, VEC> next;
+    next.load(a, row, w);
+    const Weights<VEC> wt(a, a.h != nullptr, w);
+    if (w.cl > 1) cluster_barrier();          // the other CTAs' shared memory is there
+    for (int buf = 0; row < a.n_rows; row += step, buf ^= 1) {      // the same count in all warps of a row
+        const FwdRow<XT, T, VEC> r = next;
+        next.load(a, row + step, w);
+        float xv[8], ry = 0.f;
+        if (a.y) {
+            float ss[1] = {0.f}, y[8];
+            r.y.get(y);
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss[0] = fmaf(y[i], y[i], ss[0]);
+            row_sum<1>(ss, red[buf][0], w);
+            ry = rsqrtf(ss[0] * inv_d + a.eps);                     // 1 / rms(y), times a token's gate
+            if (a.gate_mode == MOM_GATE_TOKEN) ry *= sigmoid(to_f(r.gate));
         }
-        row_sum<1>(ss, red[0], W, warp, lane);
-        const float ry = gt / sqrtf(ss[0] * inv_d + a.eps);      // 1 / rms(y), times a token's gate
+        r.x.get(xv);
+        if constexpr (!std::is_same<XT, Q8>::value) {
+            if (a.codes_out) {
+                uint32_t m[2];
+                r.x.r.amax(m);
+                act8_store<VEC>(xv, m, w.c0, d, w.lane, a.codes_out + row * d, a.scales_out + row * a.groups);
+            }
+        }
+        if (a.y) {
+            float y[8];
+            r.y.get(y);
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-            const int c0 = (warp + j * W) * kChunk;
-            float y[8], w[8];
-            yr[j].get(y);
-            xr[j].get(xv[j]);
-            if (a.codes_out)
-                act8_store<VEC>(xv[j], c0, d, lane, a.codes_out + row * d, a.scales_out + row * a.groups);
-            load8<VEC>(a.w_post, c0, d, lane, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] *= y[i] * ry;
+            for (int i = 0; i < 8; ++i) y[i] *= ry;
             if (a.gate_mode == MOM_GATE_ELEMENT) {
-                gr[j].get(y);
+                float g[8];
+                r.g.get(g);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] *= fast_sigmoid(y[i]);
+                for (int i = 0; i < 8; ++i) y[i] *= sigmoid(g[i]);
             }
-            if (a.res_scale) {
-                load8<VEC>(a.res_scale, c0, d, lane, y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) xv[j][i] = fmaf(w[i], y[i], xv[j][i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) xv[j][i] += w[i];
-            }
+            for (int i = 0; i < 8; ++i) xv[i] = fmaf(y[i], wt.post[i], xv[i]);
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < C; ++j) xr[j].load(a, row, (warp + j * W) * kChunk, lane);
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            xr[j].get(xv[j]);
-            if (a.codes_out)
-                act8_store<VEC>(xv[j], (warp + j * W) * kChunk, d, lane, a.codes_out + row * d,
-                                a.scales_out + row * a.groups);
+        if (a.x_out) {
+            if (a.x_out_f32) store8<VEC>(reinterpret_cast<float*>(a.x_out) + row * d, w.c0, d, w.lane, xv);
+            else store8<VEC>(reinterpret_cast<bf16*>(a.x_out) + row * d, w.c0, d, w.lane, xv);
         }
-    }
-    if (a.x_out) {
+        if (a.h) {
+            float ss[1] = {0.f};
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-            const int c0 = (warp + j * W) * kChunk;
-            if (a.x_out_f32) store8<VEC>(reinterpret_cast<float*>(a.x_out) + row * d, c0, d, lane, xv[j]);
-            else store8<VEC>(reinterpret_cast<bf16*>(a.x_out) + row * d, c0, d, lane, xv[j]);
-        }
-    }
-    if (a.h) {
-        float ss[1] = {0.f};
+            for (int i = 0; i < 8; ++i) ss[0] = fmaf(xv[i], xv[i], ss[0]);
+            row_sum<1>(ss, red[buf][1], w);
+            const float rx = rsqrtf(ss[0] * inv_d + a.eps);
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss[0] = fmaf(xv[j][i], xv[j][i], ss[0]);
-        row_sum<1>(ss, red[1], W, warp, lane);
-        const float rx = 1.f / sqrtf(ss[0] * inv_d + a.eps);
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            const int c0 = (warp + j * W) * kChunk;
-            float w[8];
-            load8<VEC>(a.w_pre, c0, d, lane, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] *= xv[j][i] * rx;
-            store8<VEC>(reinterpret_cast<T*>(a.h) + row * d, c0, d, lane, w);
+            for (int i = 0; i < 8; ++i) xv[i] *= rx * wt.pre[i];
+            store8<VEC>(reinterpret_cast<T*>(a.h) + row * d, w.c0, d, w.lane, xv);
         }
     }
 }
 
 // A row's operands of the adjoint, as they lie in memory.
-template <typename XT, typename T, typename G, bool VEC, int C> struct BwdRow {
-    RawX<XT, VEC> x[C];
-    Raw8<T, VEC> y[C], g[C];
-    Raw8<G, VEC> d[C], h[C];
+template <typename XT, typename T, typename G, bool VEC> struct BwdRow {
+    RawX<XT, VEC> x;
+    Raw8<T, VEC> y, g;
+    Raw8<G, VEC> d, h;
     T gate;
-    __device__ __forceinline__ void load(const ResNormArgs& a, const ResNormBwdArgs& b, int64_t row, int warp, int W,
-                                         int lane) {
+    __device__ __forceinline__ void load(const ResNormArgs& a, const ResNormBwdArgs& b, int64_t row, const Place& w) {
         if (row >= a.n_rows) return;
         const int n = a.d;
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            const int c0 = (warp + j * W) * kChunk;
-            if (a.y) y[j].load(reinterpret_cast<const T*>(a.y) + row * n, c0, n, lane);
-            x[j].load(a, row, c0, lane);
-            if (a.gate_mode == MOM_GATE_ELEMENT) g[j].load(reinterpret_cast<const T*>(a.gate) + row * n, c0, n, lane);
-            if (b.dh) h[j].load(reinterpret_cast<const G*>(b.dh) + row * n, c0, n, lane);
-            if (b.dx_out) d[j].load(reinterpret_cast<const G*>(b.dx_out) + row * n, c0, n, lane);
-        }
+        if (a.y) y.load(reinterpret_cast<const T*>(a.y) + row * n, w.c0, n, w.lane);
+        x.load(a, row, w.c0, w.lane);
+        if (a.gate_mode == MOM_GATE_ELEMENT) g.load(reinterpret_cast<const T*>(a.gate) + row * n, w.c0, n, w.lane);
+        if (b.dh) h.load(reinterpret_cast<const G*>(b.dh) + row * n, w.c0, n, w.lane);
+        if (b.dx_out) d.load(reinterpret_cast<const G*>(b.dx_out) + row * n, w.c0, n, w.lane);
         if (a.gate_mode == MOM_GATE_TOKEN) gate = reinterpret_cast<const T*>(a.gate)[row];
     }
 };
 
-// The adjoint.  A CTA walks rows blockIdx.x, + gridDim.x, ..; the next row's
-// operands are loaded (packed) before this row's arithmetic, so that loads are
-// in flight through its three reductions.  Its threads keep the two column
-// sums (A and dw_pre) of their channels in registers and write them once as
-// the CTA's partial, which cols_reduce_kernel adds up in CTA order: no
-// atomics, the same sums every time on the same device.
-template <typename XT, typename T, typename G, bool VEC, int C, int MAXW>
-__global__ void __launch_bounds__(32 * MAXW) residual_norm_bwd_kernel(const ResNormArgs a, const ResNormBwdArgs b) {
-    __shared__ float red[3][2 * kMaxWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+// The adjoint.  CTAs (clusters) walk the rows; the next row's operands are
+// loaded (packed) before this row's arithmetic, so that loads are in flight
+// through its three reductions.  Threads keep the two column sums (A and
+// dw_pre) of their channels in registers and write them once as a partial,
+// which cols_reduce_kernel adds up in order: no atomics, the same sums every
+// time on the same device.
+template <typename XT, typename T, typename G, bool VEC>
+__global__ void __launch_bounds__(32 * kWarps, 2) residual_norm_bwd_kernel(const ResNormArgs a,
+                                                                           const ResNormBwdArgs b) {
+    __shared__ float red[2][4][kMaxCluster * kWarps];
+    const Place w(a);
     const int d = a.d;
+    const int64_t step = gridDim.x / w.cl, first = blockIdx.x / w.cl;
     const float inv_d = 1.f / (float)d;
-    float accA[C][8], accP[C][8];
+    float accA[8], accP[8];
 #pragma unroll
-    for (int j = 0; j < C; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) accA[j][i] = accP[j][i] = 0.f;
-    BwdRow<XT, T, G, VEC, C> next;
-    next.load(a, b, blockIdx.x, warp, W, lane);
-    for (int64_t row = blockIdx.x; row < a.n_rows; row += gridDim.x) {
-        const BwdRow<XT, T, G, VEC, C> r = next;
-        next.load(a, b, row + gridDim.x, warp, W, lane);
-        float xv[C][8], yv[C][8], gv[C][8], dv[C][8], hv[C][8];
-        float gt = 1.f;
-        if (a.gate_mode == MOM_GATE_TOKEN) gt = fast_sigmoid(to_f(r.gate));
-        float ry = 0.f;
+    for (int i = 0; i < 8; ++i) accA[i] = accP[i] = 0.f;
+    BwdRow<XT, T, G, VEC> next;
+    next.load(a, b, first, w);
+    const Weights<VEC> wt(a, b.dh != nullptr, w);
+    if (w.cl > 1) cluster_barrier();          // the other CTAs' shared memory is there
+    int buf = 0;
+    for (int64_t row = first; row < a.n_rows; row += step, buf ^= 1) {
+        const BwdRow<XT, T, G, VEC> r = next;
+        next.load(a, b, row + step, w);
+        float yv[8], gv[8], dv[8];
+        float gt = 1.f, rest = 0.f, ry = 0.f;
+        if (a.gate_mode == MOM_GATE_TOKEN) gt = sigmoid(to_f(r.gate), rest);
         if (a.y) {
             float ss[1] = {0.f};
+            r.y.get(yv);
 #pragma unroll
-            for (int j = 0; j < C; ++j) {
-                r.y[j].get(yv[j]);
+            for (int i = 0; i < 8; ++i) ss[0] = fmaf(yv[i], yv[i], ss[0]);
+            row_sum<1>(ss, red[buf][0], w);
+            ry = rsqrtf(ss[0] * inv_d + a.eps);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss[0] = fmaf(yv[j][i], yv[j][i], ss[0]);
-            }
-            row_sum<1>(ss, red[0], W, warp, lane);
-            ry = 1.f / sqrtf(ss[0] * inv_d + a.eps);
+            for (int i = 0; i < 8; ++i) yv[i] *= ry;                          // n_y
+            if (a.gate_mode == MOM_GATE_ELEMENT) {
+                r.g.get(gv);
 #pragma unroll
-            for (int j = 0; j < C; ++j) {
-                if (a.gate_mode == MOM_GATE_ELEMENT) r.g[j].get(gv[j]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    yv[j][i] *= ry;                                       // n_y
-                    gv[j][i] = a.gate_mode == MOM_GATE_ELEMENT ? fast_sigmoid(gv[j][i]) : gt;
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            if (b.dx_out) {
-                r.d[j].get(dv[j]);
+                for (int i = 0; i < 8; ++i) gv[i] = sigmoid(gv[i]);
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dv[j][i] = 0.f;
+                for (int i = 0; i < 8; ++i) gv[i] = gt;
             }
+        }
+        if (b.dx_out) {
+            r.d.get(dv);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dv[i] = 0.f;
         }
         if (b.dh) {
-            float ss[2] = {0.f, 0.f};
+            float ss[2] = {0.f, 0.f}, xv[8], hv[8];
+            r.x.get(xv);
+            r.h.get(hv);
+            if (a.y) {
 #pragma unroll
-            for (int j = 0; j < C; ++j) {
-                const int c0 = (warp + j * W) * kChunk;
-                float w[8];
-                r.x[j].get(xv[j]);
-                r.h[j].get(hv[j]);
-                if (a.y) {
-                    load8<VEC>(a.w_post, c0, d, lane, w);
-                    if (a.res_scale) {
-                        float s[8];
-                        load8<VEC>(a.res_scale, c0, d, lane, s);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) w[i] *= s[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) xv[j][i] = fmaf(yv[j][i] * gv[j][i], w[i], xv[j][i]);   // x'
-                }
-                load8<VEC>(a.w_pre, c0, d, lane, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ss[0] = fmaf(xv[j][i], xv[j][i], ss[0]);
-                    ss[1] = fmaf(xv[j][i], hv[j][i] * w[i], ss[1]);
-                }
+                for (int i = 0; i < 8; ++i) xv[i] = fmaf(yv[i] * gv[i], wt.post[i], xv[i]);      // x'
             }
-            row_sum<2>(ss, red[1], W, warp, lane);
-            const float rx = 1.f / sqrtf(ss[0] * inv_d + a.eps);
-            const float k = ss[1] * inv_d * rx * rx;                      // mean(dn n_x) / rms
 #pragma unroll
-            for (int j = 0; j < C; ++j) {
-                float w[8];
-                load8<VEC>(a.w_pre, (warp + j * W) * kChunk, d, lane, w);
+            for (int i = 0; i < 8; ++i) {
+                ss[0] = fmaf(xv[i], xv[i], ss[0]);
+                ss[1] = fmaf(xv[i], hv[i] * wt.pre[i], ss[1]);
+            }
+            row_sum<2>(ss, red[buf][1], w);
+            const float rx = rsqrtf(ss[0] * inv_d + a.eps);
+            const float k = ss[1] * inv_d * rx * rx * rx;                     // mean(dn n_x) / rms / rms
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    accP[j][i] = fmaf(hv[j][i], xv[j][i] * rx, accP[j][i]);
-                    dv[j][i] = fmaf(fmaf(hv[j][i], w[i], -xv[j][i] * k), rx, dv[j][i]);
-                }
+            for (int i = 0; i < 8; ++i) {
+                const float hr = hv[i] * rx;
+                accP[i] = fmaf(hr, xv[i], accP[i]);
+                dv[i] = fmaf(hr, wt.pre[i], fmaf(xv[i], -k, dv[i]));
             }
         }
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-            store8<VEC>(reinterpret_cast<G*>(b.dx) + row * d, (warp + j * W) * kChunk, d, lane, dv[j]);
+        store8<VEC>(reinterpret_cast<G*>(b.dx) + row * d, w.c0, d, w.lane, dv);
         if (a.y) {
-            float ss[1] = {0.f};
+            float ss[1] = {0.f}, o[8];
 #pragma unroll
-            for (int j = 0; j < C; ++j) {
-                const int c0 = (warp + j * W) * kChunk;
-                float w[8];
-                load8<VEC>(a.w_post, c0, d, lane, w);
-                if (a.res_scale) {
-                    float s[8];
-                    load8<VEC>(a.res_scale, c0, d, lane, s);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] *= s[i];
-                }
+            for (int i = 0; i < 8; ++i) {
+                const float t = dv[i] * gv[i];
+                accA[i] = fmaf(t, yv[i], accA[i]);
+                dv[i] = t * wt.post[i];                                       // u = D s sigma w_post
+                ss[0] = fmaf(dv[i], yv[i], ss[0]);
+            }
+            row_sum<1>(ss, red[buf][3], w);
+            const float m = ss[0] * inv_d * ry;
+            if (a.gate_mode == MOM_GATE_TOKEN && b.dgate && threadIdx.x == 0 && w.rank == 0)
+                reinterpret_cast<T*>(b.dgate)[row] = from_f<T>(ss[0] * rest);
+            if (a.gate_mode == MOM_GATE_ELEMENT && b.dgate) {
+                r.g.get(o);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float t = dv[j][i] * gv[j][i];
-                    accA[j][i] = fmaf(t, yv[j][i], accA[j][i]);
-                    dv[j][i] = t * w[i];                                  // u = D s sigma w_post
-                    ss[0] = fmaf(dv[j][i], yv[j][i], ss[0]);
+                    float q;
+                    sigmoid(o[i], q);
+                    o[i] = dv[i] * yv[i] * q;
                 }
+                store8<VEC>(reinterpret_cast<T*>(b.dgate) + row * d, w.c0, d, w.lane, o);
             }
-            row_sum<1>(ss, red[2], W, warp, lane);
-            const float m = ss[0] * inv_d;
-            if (a.gate_mode == MOM_GATE_TOKEN && b.dgate && threadIdx.x == 0)
-                reinterpret_cast<T*>(b.dgate)[row] = from_f<T>(ss[0] * (1.f - gt));
 #pragma unroll
-            for (int j = 0; j < C; ++j) {
-                const int c0 = (warp + j * W) * kChunk;
-                float o[8];
-                if (a.gate_mode == MOM_GATE_ELEMENT && b.dgate) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = dv[j][i] * yv[j][i] * (1.f - gv[j][i]);
-                    store8<VEC>(reinterpret_cast<T*>(b.dgate) + row * d, c0, d, lane, o);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = (dv[j][i] - yv[j][i] * m) * ry;
-                store8<VEC>(reinterpret_cast<T*>(b.dy) + row * d, c0, d, lane, o);
-            }
+            for (int i = 0; i < 8; ++i) o[i] = fmaf(dv[i], ry, -yv[i] * m);
+            store8<VEC>(reinterpret_cast<T*>(b.dy) + row * d, w.c0, d, w.lane, o);
         }
-        // the next row's sums reuse `red`
-        if (W > 1) __syncthreads();
     }
-    float* pa = b.partial + (int64_t)blockIdx.x * 2 * d;
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-        const int c0 = (warp + j * W) * kChunk;
-        store8<VEC>(pa, c0, d, lane, accA[j]);
-        store8<VEC>(pa + d, c0, d, lane, accP[j]);
-    }
+    float* pa = b.partial + first * 2 * d;
+    store8<VEC>(pa, w.c0, d, w.lane, accA);
+    store8<VEC>(pa + d, w.c0, d, w.lane, accP);
 }
 
-// Column sums of the CTAs' partials: a CTA sums 32 channels, its 8 warps a
-// strided eighth of the partials each, joined in warp order.
-__global__ void __launch_bounds__(256) cols_reduce_kernel(const float* partial, int n_part, int d, const float* w_post,
-                                                          const float* res_scale, float* dw_post, float* dres_scale,
-                                                          float* dw_pre) {
-    __shared__ float sA[8][32], sP[8][32];
+// Column sums of the CTAs' partials: a CTA sums 32 channels of one of the two
+// (blockIdx.y), its 32 warps a strided part of the partials each, joined in
+// warp order.
+__global__ void __launch_bounds__(1024) cols_reduce_kernel(const float* partial, int n_part, int d, const float* w_post,
+                                                           const float* res_scale, float* dw_post, float* dres_scale,
+                                                           float* dw_pre) {
+    __shared__ float sh[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
-    float A = 0.f, P = 0.f;
+    const int c = blockIdx.x * 32 + lane, which = blockIdx.y;
+    float v = 0.f;
     if (c < d) {
-#pragma unroll 4
-        for (int p = warp; p < n_part; p += 8) {
-            A += partial[(int64_t)p * 2 * d + c];
-            P += partial[(int64_t)p * 2 * d + d + c];
-        }
+        const float* at = partial + (int64_t)which * d + c;
+#pragma unroll 8
+        for (int p = warp; p < n_part; p += 32) v += at[(int64_t)p * 2 * d];
     }
-    sA[warp][lane] = A;
-    sP[warp][lane] = P;
+    sh[warp][lane] = v;
     __syncthreads();
-    if (warp == 0 && c < d) {
+    if (warp != 0 || c >= d) return;
 #pragma unroll
-        for (int w = 1; w < 8; ++w) { A += sA[w][lane]; P += sP[w][lane]; }
-        if (dw_post) dw_post[c] = res_scale ? A * res_scale[c] : A;
-        if (dres_scale) dres_scale[c] = A * w_post[c];
-        if (dw_pre) dw_pre[c] = P;
+    for (int w = 1; w < 32; ++w) v += sh[w][lane];
+    if (which) {
+        if (dw_pre) dw_pre[c] = v;
+    } else {
+        if (dw_post) dw_post[c] = res_scale ? v * res_scale[c] : v;
+        if (dres_scale) dres_scale[c] = v * w_post[c];
     }
 }
 
@@ -370,72 +361,91 @@ int sm_count() {
     return sms;
 }
 
-// Chunks of 256 channels a warp holds.  Forward: two up to 4096 channels (16384
-// rows of 1024, bf16, an element gate: 44 us; one 49 us, four 47 us), four
-// above, so that a row stays within 16 warps.  Adjoint, which holds five
-// operands and two column sums: one up to 2048 channels (104 us; two 122 us),
-// 16 warps an SM (32: 124 us, by spilling its registers).
-constexpr int kFwdC = 2, kBwdC = 1, kBwdWarps = 16;
-template <typename XT, typename T, bool VEC>
-void run_fwd(ResNormArgs a, cudaStream_t st) {
-    const int chunks = (int)cdiv(a.d, kChunk);
-    const int C = chunks <= 1 ? 1 : chunks <= 8 * kFwdC ? kFwdC : 4;
-    const int W = (int)cdiv(chunks, C);
-    a.warps_per_row = W;
-    const int threads = W > 1 ? 32 * W : 128;
-    const int64_t grid = W > 1 ? a.n_rows : cdiv(a.n_rows, threads / 32);
-    if (C == 1) residual_norm_kernel<XT, T, VEC, 1, 8><<<(unsigned)grid, threads, 0, st>>>(a);
-    else if (C == kFwdC) residual_norm_kernel<XT, T, VEC, kFwdC, 8><<<(unsigned)grid, threads, 0, st>>>(a);
-    else residual_norm_kernel<XT, T, VEC, 4, 16><<<(unsigned)grid, threads, 0, st>>>(a);
+// CTAs of a row's cluster and warps of a CTA.
+struct Shape {
+    int cluster, warps;
+};
+Shape shape_for(int d) {
+    const int chunks = (int)cdiv(d, kChunk);
+    int cl = 1;
+    while (cl * kWarps < chunks) cl *= 2;
+    return {cl, (int)cdiv(chunks, cl)};
+}
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), int64_t ctas, int threads, int cluster, cudaStream_t st, const A&... args) {
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = cluster;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Warps an SM: __launch_bounds__ leaves at most 128 registers a thread.
+constexpr int kWarpsSM = 16;
+
+template <typename XT, typename T, bool VEC> cudaError_t run_fwd(ResNormArgs a, cudaStream_t st) {
+    const Shape s = shape_for(a.d);
+    a.cluster = s.cluster;
+    a.warps_per_row = s.warps;
+    const bool own = s.warps * s.cluster == 1;                 // a row a warp
+    const int threads = own ? 128 : 32 * s.warps;
+    const int64_t units = own ? cdiv(a.n_rows, threads / 32) : a.n_rows;
+    const int64_t most = (int64_t)sm_count() * (kWarpsSM / (threads / 32)) / s.cluster;
+    return launch(residual_norm_kernel<XT, T, VEC>, (units < most ? units : most) * s.cluster, threads, s.cluster, st, a);
 }
 
 template <typename XT, typename T, typename G, bool VEC>
-void run_bwd(const ResNormArgs& a, const ResNormBwdArgs& b, int grid, cudaStream_t st) {
-    const int chunks = (int)cdiv(a.d, kChunk);
-    const int C = chunks <= 8 * kBwdC ? kBwdC : chunks <= 16 ? 2 : 4;
-    const int threads = 32 * (int)cdiv(chunks, C);
-    if (C == kBwdC) residual_norm_bwd_kernel<XT, T, G, VEC, kBwdC, 8><<<grid, threads, 0, st>>>(a, b);
-    else if (C == 2) residual_norm_bwd_kernel<XT, T, G, VEC, 2, 8><<<grid, threads, 0, st>>>(a, b);
-    else residual_norm_bwd_kernel<XT, T, G, VEC, 4, 16><<<grid, threads, 0, st>>>(a, b);
+cudaError_t run_bwd(ResNormArgs a, const ResNormBwdArgs& b, int parts, cudaStream_t st) {
+    const Shape s = shape_for(a.d);
+    a.cluster = s.cluster;
+    a.warps_per_row = s.warps;
+    return launch(residual_norm_bwd_kernel<XT, T, G, VEC>, (int64_t)parts * s.cluster, 32 * s.warps, s.cluster, st, a, b);
 }
 
 }  // namespace
 
 // rows of partial column sums the adjoint writes
 int residual_norm_bwd_parts(int64_t n_rows, int d) {
-    const int chunks = (int)cdiv(d, kChunk);
-    const int warps = (int)cdiv(chunks, chunks <= 8 * kBwdC ? kBwdC : chunks <= 16 ? 2 : 4);
-    const int64_t most = (int64_t)sm_count() * (warps <= kBwdWarps ? kBwdWarps / warps : 1);
+    const Shape s = shape_for(d);
+    const int64_t most = (int64_t)sm_count() * (kWarpsSM / s.warps) / s.cluster;
     return (int)(n_rows < most ? n_rows : most);
 }
 
 cudaError_t launch_residual_norm(const ResNormArgs& a, int x_kind, int dt, bool vec, cudaStream_t st) {
-#define MOM_RN(XT, T) do { if (vec) run_fwd<XT, T, true>(a, st); else run_fwd<XT, T, false>(a, st); } while (0)
+    cudaError_t e;
+#define MOM_RN(XT, T) e = vec ? run_fwd<XT, T, true>(a, st) : run_fwd<XT, T, false>(a, st)
     if (x_kind == RN_X_BF16) MOM_RN(bf16, bf16);
     else if (x_kind == RN_X_F32) { if (dt == MOM_BF16) MOM_RN(float, bf16); else MOM_RN(float, float); }
     else { if (dt == MOM_BF16) MOM_RN(Q8, bf16); else MOM_RN(Q8, float); }
 #undef MOM_RN
     count_launches(1);
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_residual_norm_bwd(const ResNormArgs& a, const ResNormBwdArgs& b, int x_kind, int dt, int g_dt,
                                      bool vec, cudaStream_t st) {
     const int parts = residual_norm_bwd_parts(a.n_rows, a.d);
     if (parts > 0) {
-#define MOM_RNB(XT, T, G) do { if (vec) run_bwd<XT, T, G, true>(a, b, parts, st); else run_bwd<XT, T, G, false>(a, b, parts, st); } while (0)
-#define MOM_RNG(XT, T) do { if (g_dt == MOM_BF16) MOM_RNB(XT, T, bf16); else MOM_RNB(XT, T, float); } while (0)
+        cudaError_t e;
+#define MOM_RNB(XT, T, G) e = vec ? run_bwd<XT, T, G, true>(a, b, parts, st) : run_bwd<XT, T, G, false>(a, b, parts, st)
+#define MOM_RNG(XT, T) do { if (g_dt == MOM_BF16) { MOM_RNB(XT, T, bf16); } else { MOM_RNB(XT, T, float); } } while (0)
         if (x_kind == RN_X_BF16) MOM_RNG(bf16, bf16);
         else if (x_kind == RN_X_F32) { if (dt == MOM_BF16) MOM_RNG(float, bf16); else MOM_RNG(float, float); }
         else { if (dt == MOM_BF16) MOM_RNG(Q8, bf16); else MOM_RNG(Q8, float); }
 #undef MOM_RNG
 #undef MOM_RNB
         count_launches(1);
-        const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     if (b.dw_post || b.dres_scale || b.dw_pre) {
-        cols_reduce_kernel<<<(unsigned)cdiv(a.d, 32), 256, 0, st>>>(b.partial, parts, a.d, a.w_post, a.res_scale,
+        cols_reduce_kernel<<<dim3((unsigned)cdiv(a.d, 32), 2), 1024, 0, st>>>(b.partial, parts, a.d, a.w_post, a.res_scale,
                                                                     b.dw_post, b.dres_scale, b.dw_pre);
         count_launches(1);
     }

@@ -15,9 +15,17 @@ constexpr int kChunk = 256;                   // channels of a warp's chunk
 constexpr int kActGroup = MOM_ACT8_GROUP;     // channels that share a scale
 static_assert(kChunk == 2 * kActGroup, "a chunk holds two groups");
 
-// channel of element i of lane l, from the chunk's first channel
-template <bool VEC> __device__ __forceinline__ int chunk_col(int lane, int i) {
-    return VEC ? lane * 8 + i : i * 32 + lane;
+// The hardware reciprocal and exponential (one and two ulps; tiny results are
+// flushed to 0): a rounded division took 15 of an element's 50 instructions.
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float fast_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // A lane's 8 channels of a row as they lie in memory (channels >= d give 0):
@@ -37,6 +45,12 @@ template <typename T, bool VEC> struct Raw8 {
 #pragma unroll
         for (int i = 0; i < 8; ++i) out[i] = v[i];
     }
+    // largest magnitude's bits of the lane's elements of each group
+    __device__ __forceinline__ void amax(uint32_t (&m)[2]) const {
+        m[0] = m[1] = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i >> 2] = max(m[i >> 2], __float_as_uint(v[i]) & 0x7fffffffu);
+    }
 };
 template <> struct Raw8<bf16, true> {
     uint4 u;
@@ -52,6 +66,11 @@ template <> struct Raw8<bf16, true> {
             out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
+    __device__ __forceinline__ void amax(uint32_t (&m)[2]) const {      // two elements an instruction
+        const uint32_t a = 0x7fff7fffu;
+        const uint32_t t = __vmaxu2(__vmaxu2(u.x & a, u.y & a), __vmaxu2(u.z & a, u.w & a));
+        m[0] = m[1] = max(t << 16, t & 0xffff0000u);
+    }
 };
 template <> struct Raw8<float, true> {
     float4 a, b;
@@ -63,6 +82,14 @@ template <> struct Raw8<float, true> {
     __device__ __forceinline__ void get(float* out) const {
         out[0] = a.x; out[1] = a.y; out[2] = a.z; out[3] = a.w;
         out[4] = b.x; out[5] = b.y; out[6] = b.z; out[7] = b.w;
+    }
+    __device__ __forceinline__ void amax(uint32_t (&m)[2]) const {
+        float v[8];
+        get(v);
+        m[0] = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[0] = max(m[0], __float_as_uint(v[i]) & 0x7fffffffu);
+        m[1] = m[0];
     }
 };
 
@@ -99,22 +126,18 @@ __device__ __forceinline__ void store8(T* row, int c0, int d, int lane, const fl
 // scale, so that all of it restores to NaN.
 constexpr float kRoundMagic = 12582912.f;                     // 1.5 * 2^23
 
+// fl32(a / 127): the product with 1/127 and one correction by its remainder,
+// which gives the rounded quotient of every float a >= 2^-100 (all mantissas
+// were compared with the division).
 __device__ __forceinline__ float act8_scale(uint32_t amax_bits) {
     if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
-    const float a = __uint_as_float(amax_bits);
-    return a < 7.888609052210118e-31f ? 0.f : a / 127.f;      // 2^-100
+    const float a = __uint_as_float(amax_bits), r = 1.f / 127.f, q = a * r;
+    return a < 7.888609052210118e-31f ? 0.f : fmaf(fmaf(-127.f, q, a), r, q);      // 2^-100
 }
 
-// The two groups' scales of a chunk held in v (lane layout above): the scale of
+// The two groups' scales of a chunk from the lanes' maxima: the scale of
 // element i in s[i >= 4] (VEC: both entries are the lane's own group's).
-template <bool VEC> __device__ __forceinline__ void act8_scales(const float* v, float (&s)[2]) {
-    uint32_t m[2] = {0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
-        if constexpr (VEC) m[0] = max(m[0], b);
-        else m[i >> 2] = max(m[i >> 2], b);
-    }
+template <bool VEC> __device__ __forceinline__ void act8_scales(uint32_t (&m)[2], float (&s)[2]) {
     if constexpr (VEC) {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
@@ -127,8 +150,8 @@ template <bool VEC> __device__ __forceinline__ void act8_scales(const float* v, 
 
 // The codes of a lane's 8 elements, in the low byte of q[i].
 __device__ __forceinline__ void act8_codes(const float* v, const float (&s)[2], uint32_t* q) {
-    // 1 / scale: at most two ulps off, which the remainder puts right
-    const float inv[2] = {s[0] > 0.f ? __fdividef(1.f, s[0]) : 0.f, s[1] > 0.f ? __fdividef(1.f, s[1]) : 0.f};
+    // 1 / scale: an ulp off, which the remainder puts right (scale 0: the product is not used)
+    const float inv[2] = {fast_rcp(s[0]), fast_rcp(s[1])};
     bool fix = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -151,12 +174,13 @@ __device__ __forceinline__ void act8_codes(const float* v, const float (&s)[2], 
 }
 
 // Codes and scales of a chunk out: codes_row [d], scales_row [ceil(d / 128)].
+// v: the lane's elements, m: their groups' maxima (Raw8::amax).
 template <bool VEC>
-__device__ __forceinline__ void act8_store(const float* v, int c0, int d, int lane, int8_t* codes_row,
-                                           float* scales_row) {
+__device__ __forceinline__ void act8_store(const float* v, uint32_t (&m)[2], int c0, int d, int lane,
+                                           int8_t* codes_row, float* scales_row) {
     float s[2];
     uint32_t q[8];
-    act8_scales<VEC>(v, s);
+    act8_scales<VEC>(m, s);
     act8_codes(v, s, q);
     const int g0 = c0 / kActGroup;
     if constexpr (VEC) {

@@ -24,14 +24,22 @@ namespace mom {
 namespace {
 
 template <typename XT, bool VEC> struct RawX {
-    Raw8<XT, VEC> r;
+    typedef Raw8<XT, VEC> R;
+    R r;
+    static __device__ __forceinline__ void copy(uint32_t slot, uint32_t pitch, const ResNormArgs& a, int64_t row, int c0, int lane) {
+        R::copy(slot, pitch, reinterpret_cast<const XT*>(a.x) + row * a.d, c0, a.d, lane);
+    }
     __device__ __forceinline__ void load(const ResNormArgs& a, int64_t row, int c0, int lane) {
         r.load(reinterpret_cast<const XT*>(a.x) + row * a.d, c0, a.d, lane);
     }
     __device__ __forceinline__ void get(float* out) const { r.get(out); }
 };
 template <bool VEC> struct RawX<Q8, VEC> {
-    Raw8Q<VEC> r;
+    typedef Raw8Q<VEC> R;
+    R r;
+    static __device__ __forceinline__ void copy(uint32_t slot, uint32_t pitch, const ResNormArgs& a, int64_t row, int c0, int lane) {
+        R::copy(slot, pitch, a.x_codes + row * a.d, a.x_scales + row * a.groups, c0, a.d, lane);
+    }
     __device__ __forceinline__ void load(const ResNormArgs& a, int64_t row, int c0, int lane) {
         r.load(a.x_codes + row * a.d, a.x_scales + row * a.groups, c0, a.d, lane);
     }
@@ -118,47 +126,107 @@ template <bool VEC> struct Weights {
 };
 
 // A row's operands of the forward, as they lie in memory.
-template <typename XT, typename T, bool VEC> struct FwdRow {
+template <typename XT, typename T, bool VEC, bool HAS_Y> struct FwdRow {
     RawX<XT, VEC> x;
     Raw8<T, VEC> y, g;
-    T gate;
     __device__ __forceinline__ void load(const ResNormArgs& a, int64_t row, const Place& w) {
         if (row >= a.n_rows) return;
-        if (a.y) y.load(reinterpret_cast<const T*>(a.y) + row * a.d, w.c0, a.d, w.lane);
+        if (HAS_Y) y.load(reinterpret_cast<const T*>(a.y) + row * a.d, w.c0, a.d, w.lane);
         x.load(a, row, w.c0, w.lane);
-        if (a.gate_mode == MOM_GATE_ELEMENT) g.load(reinterpret_cast<const T*>(a.gate) + row * a.d, w.c0, a.d, w.lane);
-        if (a.gate_mode == MOM_GATE_TOKEN) gate = reinterpret_cast<const T*>(a.gate)[row];
+        if (HAS_Y && a.gate_mode == MOM_GATE_ELEMENT)
+            g.load(reinterpret_cast<const T*>(a.gate) + row * a.d, w.c0, a.d, w.lane);
     }
 };
 
-// CTAs (clusters; warps, with one warp a row) walk the rows, the next one's
-// operands loaded before this one's arithmetic.  `red` alternates between two
-// rows, so that one barrier a sum is enough.
-template <typename XT, typename T, bool VEC>
-__global__ void __launch_bounds__(32 * kWarps, 2) residual_norm_kernel(const ResNormArgs a) {
+// Rows of the forward ahead of the one at work: copies in flight to a ring of
+// slots in shared memory, of which each thread reads only what it copied (no
+// barrier).  A slot is filled again one row after it was read.  Without a
+// block's output a row is short, so more rows are ahead.  Rows that 16-byte
+// copies cannot take are loaded one ahead into registers.
+template <typename XT, typename T, bool VEC, bool HAS_Y> struct FwdRing {
+    static constexpr int AHEAD = HAS_Y ? 2 : 6, SLOTS = AHEAD + 1;
+    typedef FwdRow<XT, T, VEC, HAS_Y> Row;
+    uint32_t base, pitch, bytes;
+    int in, out;
+    static __host__ __device__ constexpr int pieces(bool elem) {
+        return RawX<XT, true>::R::PIECES + (HAS_Y ? (elem ? 2 : 1) * Raw8<T, true>::PIECES : 0);
+    }
+    __device__ __forceinline__ FwdRing(const ResNormArgs& a, void* smem) {
+        pitch = blockDim.x * 16;
+        base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+        bytes = pieces(a.gate_mode == MOM_GATE_ELEMENT) * pitch;
+        in = out = 0;
+    }
+    __device__ __forceinline__ void put(const ResNormArgs& a, int64_t row, const Place& w) {
+        if (row < a.n_rows) {
+            uint32_t at = base + in * bytes;
+            RawX<XT, VEC>::copy(at, pitch, a, row, w.c0, w.lane);
+            at += RawX<XT, VEC>::R::PIECES * pitch;
+            if (HAS_Y) Raw8<T, VEC>::copy(at, pitch, reinterpret_cast<const T*>(a.y) + row * a.d, w.c0, a.d, w.lane);
+            at += Raw8<T, VEC>::PIECES * pitch;
+            if (HAS_Y && a.gate_mode == MOM_GATE_ELEMENT)
+                Raw8<T, VEC>::copy(at, pitch, reinterpret_cast<const T*>(a.gate) + row * a.d, w.c0, a.d, w.lane);
+        }
+        in = in + 1 == SLOTS ? 0 : in + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ void take(const ResNormArgs& a, Row& r) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+        uint32_t at = base + out * bytes;
+        r.x.r.take(at, pitch);
+        at += RawX<XT, VEC>::R::PIECES * pitch;
+        if (HAS_Y) r.y.take(at, pitch);
+        at += Raw8<T, VEC>::PIECES * pitch;
+        if (HAS_Y && a.gate_mode == MOM_GATE_ELEMENT) r.g.take(at, pitch);
+        out = out + 1 == SLOTS ? 0 : out + 1;
+    }
+};
+template <typename XT, typename T, bool HAS_Y> struct FwdRing<XT, T, false, HAS_Y> {
+    typedef FwdRow<XT, T, false, HAS_Y> Row;
+    static constexpr int AHEAD = 1, SLOTS = 0;
+    Row next;
+    static constexpr int pieces(bool) { return 0; }
+    __device__ __forceinline__ FwdRing(const ResNormArgs&, void*) {}
+    __device__ __forceinline__ void put(const ResNormArgs& a, int64_t row, const Place& w) { next.load(a, row, w); }
+    __device__ __forceinline__ void take(const ResNormArgs&, Row& r) { r = next; }
+};
+
+// CTAs (clusters; warps, with one warp a row) walk the rows.  `red` alternates
+// between two rows, so that one barrier a sum is enough.
+template <typename XT, typename T, bool VEC, bool HAS_Y>
+__global__ void __launch_bounds__(32 * kWarps, VEC ? 3 : 2) residual_norm_kernel(const ResNormArgs a) {
+    extern __shared__ __align__(16) unsigned char slots[];
     __shared__ float red[2][2][kMaxCluster * kWarps];
+    typedef FwdRing<XT, T, VEC, HAS_Y> Ring;
     const Place w(a);
     const int rows_cta = w.W > 1 ? 1 : blockDim.x >> 5;
     const int64_t step = (int64_t)gridDim.x / w.cl * rows_cta;
     int64_t row = (int64_t)(blockIdx.x / w.cl) * rows_cta + (w.W > 1 ? 0 : threadIdx.x >> 5);
     const int d = a.d;
     const float inv_d = 1.f / (float)d;
-    FwdRow<XT, T, VEC> next;
-    next.load(a, row, w);
+    Ring ring(a, slots);
+#pragma unroll
+    for (int i = 0; i < Ring::AHEAD; ++i) ring.put(a, row + i * step, w);
+    T gate_next = from_f<T>(0.f);
+    if (a.gate_mode == MOM_GATE_TOKEN && row < a.n_rows) gate_next = reinterpret_cast<const T*>(a.gate)[row];
     const Weights<VEC> wt(a, a.h != nullptr, w);
     if (w.cl > 1) cluster_barrier();          // the other CTAs' shared memory is there
     for (int buf = 0; row < a.n_rows; row += step, buf ^= 1) {      // the same count in all warps of a row
-        const FwdRow<XT, T, VEC> r = next;
-        next.load(a, row + step, w);
+        FwdRow<XT, T, VEC, HAS_Y> r;
+        ring.take(a, r);
+        ring.put(a, row + Ring::AHEAD * step, w);
+        const T gate = gate_next;
+        if (a.gate_mode == MOM_GATE_TOKEN && row + step < a.n_rows)
+            gate_next = reinterpret_cast<const T*>(a.gate)[row + step];
         float xv[8], ry = 0.f;
-        if (a.y) {
+        if (HAS_Y) {
             float ss[1] = {0.f}, y[8];
             r.y.get(y);
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss[0] = fmaf(y[i], y[i], ss[0]);
             row_sum<1>(ss, red[buf][0], w);
             ry = rsqrtf(ss[0] * inv_d + a.eps);                     // 1 / rms(y), times a token's gate
-            if (a.gate_mode == MOM_GATE_TOKEN) ry *= sigmoid(to_f(r.gate));
+            if (a.gate_mode == MOM_GATE_TOKEN) ry *= sigmoid(to_f(gate));
         }
         r.x.get(xv);
         if constexpr (!std::is_same<XT, Q8>::value) {
@@ -168,7 +236,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) residual_norm_kernel(const Res
                 act8_store<VEC>(xv, m, w.c0, d, w.lane, a.codes_out + row * d, a.scales_out + row * a.groups);
             }
         }
-        if (a.y) {
+        if (HAS_Y) {
             float y[8];
             r.y.get(y);
 #pragma unroll
@@ -373,7 +441,8 @@ Shape shape_for(int d) {
 }
 
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), int64_t ctas, int threads, int cluster, cudaStream_t st, const A&... args) {
+cudaError_t launch(void (*kernel)(P...), int64_t ctas, int threads, size_t smem, int cluster, cudaStream_t st,
+                   const A&... args) {
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = cluster;
@@ -381,24 +450,34 @@ cudaError_t launch(void (*kernel)(P...), int64_t ctas, int threads, int cluster,
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = &at;
     cfg.numAttrs = cluster > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Warps an SM: __launch_bounds__ leaves at most 128 registers a thread.
-constexpr int kWarpsSM = 16;
+// Warps an SM that the registers leave (__launch_bounds__).
+constexpr int kFwdWarps = 24, kWarpsSM = 16;
+constexpr int kSmemSM = 220 * 1024;
 
-template <typename XT, typename T, bool VEC> cudaError_t run_fwd(ResNormArgs a, cudaStream_t st) {
+template <typename XT, typename T, bool VEC, bool HAS_Y> cudaError_t run_fwd(ResNormArgs a, cudaStream_t st) {
+    typedef FwdRing<XT, T, VEC, HAS_Y> Ring;
+    auto* kernel = residual_norm_kernel<XT, T, VEC, HAS_Y>;
     const Shape s = shape_for(a.d);
     a.cluster = s.cluster;
     a.warps_per_row = s.warps;
     const bool own = s.warps * s.cluster == 1;                 // a row a warp
     const int threads = own ? 128 : 32 * s.warps;
+    const size_t smem = (size_t)Ring::SLOTS * Ring::pieces(a.gate_mode == MOM_GATE_ELEMENT) * threads * 16;
+    static unsigned long long optin_done = 0;
+    const cudaError_t e = smem_optin((const void*)kernel, Ring::SLOTS * Ring::pieces(true) * 32 * kWarps * 16, &optin_done);
+    if (e != cudaSuccess) return e;
+    int ctas = (VEC ? kFwdWarps : kWarpsSM) / (threads / 32);
+    if (smem * ctas > kSmemSM) ctas = (int)(kSmemSM / smem);
     const int64_t units = own ? cdiv(a.n_rows, threads / 32) : a.n_rows;
-    const int64_t most = (int64_t)sm_count() * (kWarpsSM / (threads / 32)) / s.cluster;
-    return launch(residual_norm_kernel<XT, T, VEC>, (units < most ? units : most) * s.cluster, threads, s.cluster, st, a);
+    const int64_t most = (int64_t)sm_count() * ctas / s.cluster;
+    return launch(kernel, (units < most ? units : most) * s.cluster, threads, smem, s.cluster, st, a);
 }
 
 template <typename XT, typename T, typename G, bool VEC>
@@ -406,7 +485,7 @@ cudaError_t run_bwd(ResNormArgs a, const ResNormBwdArgs& b, int parts, cudaStrea
     const Shape s = shape_for(a.d);
     a.cluster = s.cluster;
     a.warps_per_row = s.warps;
-    return launch(residual_norm_bwd_kernel<XT, T, G, VEC>, (int64_t)parts * s.cluster, 32 * s.warps, s.cluster, st, a, b);
+    return launch(residual_norm_bwd_kernel<XT, T, G, VEC>, (int64_t)parts * s.cluster, 32 * s.warps, 0, s.cluster, st, a, b);
 }
 
 }  // namespace
@@ -420,7 +499,8 @@ int residual_norm_bwd_parts(int64_t n_rows, int d) {
 
 cudaError_t launch_residual_norm(const ResNormArgs& a, int x_kind, int dt, bool vec, cudaStream_t st) {
     cudaError_t e;
-#define MOM_RN(XT, T) e = vec ? run_fwd<XT, T, true>(a, st) : run_fwd<XT, T, false>(a, st)
+#define MOM_RN(XT, T) e = a.y ? (vec ? run_fwd<XT, T, true, true>(a, st) : run_fwd<XT, T, false, true>(a, st)) \
+                        : (vec ? run_fwd<XT, T, true, false>(a, st) : run_fwd<XT, T, false, false>(a, st))
     if (x_kind == RN_X_BF16) MOM_RN(bf16, bf16);
     else if (x_kind == RN_X_F32) { if (dt == MOM_BF16) MOM_RN(float, bf16); else MOM_RN(float, float); }
     else { if (dt == MOM_BF16) MOM_RN(Q8, bf16); else MOM_RN(Q8, float); }

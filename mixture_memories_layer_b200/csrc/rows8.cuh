@@ -11,6 +11,17 @@
 
 namespace mom {
 
+// 16-byte pieces that a thread keeps for itself in shared memory while their
+// copies are in flight: piece p of a slot at slot + p * pitch, pitch = threads * 16.
+__device__ __forceinline__ void piece_copy16(uint32_t dst, const void* src, bool in) {      // else zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 piece_read(uint32_t at) {
+    uint4 u;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
+    return u;
+}
+
 constexpr int kChunk = 256;                   // channels of a warp's chunk
 constexpr int kActGroup = MOM_ACT8_GROUP;     // channels that share a scale
 static_assert(kChunk == 2 * kActGroup, "a chunk holds two groups");
@@ -53,11 +64,17 @@ template <typename T, bool VEC> struct Raw8 {
     }
 };
 template <> struct Raw8<bf16, true> {
+    static constexpr int PIECES = 1;
     uint4 u;
     __device__ __forceinline__ void load(const bf16* row, int c0, int d, int lane) {
         const int c = c0 + lane * 8;
         u = c < d ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
     }
+    static __device__ __forceinline__ void copy(uint32_t slot, uint32_t, const bf16* row, int c0, int d, int lane) {
+        const int c = c0 + lane * 8;
+        piece_copy16(slot, row + (c < d ? c : 0), c < d);
+    }
+    __device__ __forceinline__ void take(uint32_t slot, uint32_t) { u = piece_read(slot); }
     __device__ __forceinline__ void get(float* out) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -73,7 +90,18 @@ template <> struct Raw8<bf16, true> {
     }
 };
 template <> struct Raw8<float, true> {
+    static constexpr int PIECES = 2;
     float4 a, b;
+    static __device__ __forceinline__ void copy(uint32_t slot, uint32_t pitch, const float* row, int c0, int d, int lane) {
+        const int c = c0 + lane * 8;
+        piece_copy16(slot, row + (c < d ? c : 0), c < d);
+        piece_copy16(slot + pitch, row + (c < d ? c + 4 : 0), c < d);
+    }
+    __device__ __forceinline__ void take(uint32_t slot, uint32_t pitch) {
+        const uint4 u = piece_read(slot), v = piece_read(slot + pitch);
+        a = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+        b = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+    }
     __device__ __forceinline__ void load(const float* row, int c0, int d, int lane) {
         const int c = c0 + lane * 8;
         a = c < d ? *reinterpret_cast<const float4*>(row + c) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -207,8 +235,23 @@ __device__ __forceinline__ void act8_store(const float* v, uint32_t (&m)[2], int
 struct Q8 {};                  // the stream's type tag where it is a checkpoint
 template <bool VEC> struct Raw8Q;
 template <> struct Raw8Q<true> {
+    static constexpr int PIECES = 1;       // 8 bytes of codes, the scale behind them
     uint2 u;
     float s;
+    static __device__ __forceinline__ void copy(uint32_t slot, uint32_t, const int8_t* codes_row, const float* scales_row,
+                                                int c0, int d, int lane) {
+        const int c = c0 + lane * 8;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;"
+                     ::"r"(slot), "l"(codes_row + (c < d ? c : 0)), "r"(c < d ? 8 : 0) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                     ::"r"(slot + 8), "l"(scales_row + (c < d ? c0 / kActGroup + (lane >> 4) : 0)), "r"(c < d ? 4 : 0)
+                     : "memory");
+    }
+    __device__ __forceinline__ void take(uint32_t slot, uint32_t) {
+        const uint4 p = piece_read(slot);
+        u = make_uint2(p.x, p.y);
+        s = __uint_as_float(p.z);
+    }
     __device__ __forceinline__ void load(const int8_t* codes_row, const float* scales_row, int c0, int d, int lane) {
         const int c = c0 + lane * 8;
         u = make_uint2(0u, 0u);

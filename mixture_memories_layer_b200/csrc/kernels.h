@@ -303,7 +303,7 @@ struct ResNormArgs {
     int x_out_f32;
     int8_t* codes_out;
     float* scales_out;
-    int warps_per_row, cluster;    // set by the launcher
+    int warps_per_row;             // set by the launcher
 };
 struct ResNormBwdArgs {
     const void *dx_out, *dh;       // gradient type

@@ -23,27 +23,26 @@
 namespace mom {
 namespace {
 
-template <typename XT, bool VEC> struct RawX {
+// The stream's operand: a type's elements or an 8-bit checkpoint.
+template <typename XT, bool VEC> struct RawX : Raw8<XT, VEC> {
     typedef Raw8<XT, VEC> R;
-    R r;
-    static __device__ __forceinline__ void copy(uint32_t slot, uint32_t pitch, const ResNormArgs& a, int64_t row, int c0, int lane) {
+    __device__ __forceinline__ void load(const ResNormArgs& a, int64_t row, int c0, int lane) {
+        R::load(reinterpret_cast<const XT*>(a.x) + row * a.d, c0, a.d, lane);
+    }
+    static __device__ __forceinline__ void copy(uint32_t slot, uint32_t pitch, const ResNormArgs& a, int64_t row, int c0,
+                                                int lane) {
         R::copy(slot, pitch, reinterpret_cast<const XT*>(a.x) + row * a.d, c0, a.d, lane);
     }
-    __device__ __forceinline__ void load(const ResNormArgs& a, int64_t row, int c0, int lane) {
-        r.load(reinterpret_cast<const XT*>(a.x) + row * a.d, c0, a.d, lane);
-    }
-    __device__ __forceinline__ void get(float* out) const { r.get(out); }
 };
-template <bool VEC> struct RawX<Q8, VEC> {
+template <bool VEC> struct RawX<Q8, VEC> : Raw8Q<VEC> {
     typedef Raw8Q<VEC> R;
-    R r;
-    static __device__ __forceinline__ void copy(uint32_t slot, uint32_t pitch, const ResNormArgs& a, int64_t row, int c0, int lane) {
+    __device__ __forceinline__ void load(const ResNormArgs& a, int64_t row, int c0, int lane) {
+        R::load(a.x_codes + row * a.d, a.x_scales + row * a.groups, c0, a.d, lane);
+    }
+    static __device__ __forceinline__ void copy(uint32_t slot, uint32_t pitch, const ResNormArgs& a, int64_t row, int c0,
+                                                int lane) {
         R::copy(slot, pitch, a.x_codes + row * a.d, a.x_scales + row * a.groups, c0, a.d, lane);
     }
-    __device__ __forceinline__ void load(const ResNormArgs& a, int64_t row, int c0, int lane) {
-        r.load(a.x_codes + row * a.d, a.x_scales + row * a.groups, c0, a.d, lane);
-    }
-    __device__ __forceinline__ void get(float* out) const { r.get(out); }
 };
 
 // sigma(z) = 1 / (1 + e), e = exp(-z), by the hardware exponential and
@@ -56,342 +55,466 @@ __device__ __forceinline__ float sigmoid(float z, float& rest) {
 }
 __device__ __forceinline__ float sigmoid(float z) { return fast_rcp(1.f + fast_ex2(z * -1.4426950408889634f)); }
 
-constexpr int kWarps = 8;        // warps of a row's CTA; wider rows take a cluster of CTAs
-constexpr int kMaxCluster = 8;
-static_assert(kMaxCluster * kWarps * kChunk >= MOM_NORM_MAX_D, "a cluster holds a row");
+constexpr int kMaxWarps = 16;      // of a row
 
-// Who holds what of a row: W warps a CTA with one chunk of 256 channels each,
-// in `cl` CTAs.  One warp a row: every warp of the CTA has its own.
-struct Place {
-    int lane, W, warp, cl, rank, c0;
-    __device__ __forceinline__ Place(const ResNormArgs& a) {
-        lane = threadIdx.x & 31;
-        W = a.warps_per_row;
-        warp = W > 1 ? threadIdx.x >> 5 : 0;
-        cl = a.cluster;
-        asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-        c0 = (rank * W + warp) * kChunk;
-    }
-};
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Sums of K values over a row (every thread gets them), in warp order.  One
-// warp a row needs no barrier; in a cluster each warp writes its sums to every
-// CTA's shared memory and one cluster barrier takes the place of the CTA's.
-template <int K> __device__ __forceinline__ void row_sum(float (&v)[K], float* buf, const Place& w) {
+// Sums of K values over the W warps of a row (every thread gets them), in warp
+// order; one warp a row needs no barrier.
+template <int K> __device__ __forceinline__ void row_sum(float (&v)[K], float* buf, int W, int warp, int lane) {
     warp_sum_n<K>(v);
-    if (w.W * w.cl == 1) return;
-    if (w.cl > 1) {
-        if (w.lane < w.cl) {
-            uint32_t at;
-            asm("mapa.shared::cluster.u32 %0, %1, %2;"
-                : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(buf)), "r"(w.lane));
+    if (W == 1) return;
+    if (lane == 0)
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                asm volatile("st.shared::cluster.f32 [%0], %1;"
-                             ::"r"(at + 4 * ((w.rank * w.W + w.warp) * K + k)), "f"(v[k]) : "memory");
-        }
-        cluster_barrier();
-    } else {
-        if (w.lane == 0)
-#pragma unroll
-            for (int k = 0; k < K; ++k) buf[w.warp * K + k] = v[k];
-        __syncthreads();
-    }
+        for (int k = 0; k < K; ++k) buf[warp * K + k] = v[k];
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = 0.f;
-    for (int i = 0; i < w.W * w.cl; ++i)
+    for (int i = 0; i < W; ++i)
 #pragma unroll
         for (int k = 0; k < K; ++k) v[k] += buf[i * K + k];
 }
 
-// The column weights of a thread's channels, res_scale * w_post and w_pre, in
-// registers for all of a CTA's rows.
-template <bool VEC> struct Weights {
-    float post[8], pre[8];
-    __device__ __forceinline__ Weights(const ResNormArgs& a, bool has_pre, const Place& w) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) post[i] = pre[i] = 0.f;
-        if (a.y) load8<VEC>(a.w_post, w.c0, a.d, w.lane, post);
-        if (a.y && a.res_scale) {
+// The column weights of a thread's channels, res_scale * w_post and w_pre: in
+// registers for all of a CTA's rows with one chunk a warp, else read again
+// (from L1) at each use.
+template <bool VEC, int C> struct Weights {
+    static constexpr bool KEEP = C == 1;
+    float post[KEEP ? 8 : 1], pre[KEEP ? 8 : 1];
+    static __device__ __forceinline__ void read_post(const ResNormArgs& a, int c0, int lane, float* w) {
+        load8<VEC>(a.w_post, c0, a.d, lane, w);
+        if (a.res_scale) {
             float s[8];
-            load8<VEC>(a.res_scale, w.c0, a.d, w.lane, s);
+            load8<VEC>(a.res_scale, c0, a.d, lane, s);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) post[i] *= s[i];
+            for (int i = 0; i < 8; ++i) w[i] *= s[i];
         }
-        if (has_pre) load8<VEC>(a.w_pre, w.c0, a.d, w.lane, pre);
+    }
+    __device__ __forceinline__ Weights(const ResNormArgs& a, bool has_pre, int c0, int lane) {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) post[i] = pre[i] = 0.f;
+            if (a.y) read_post(a, c0, lane, post);
+            if (has_pre) load8<VEC>(a.w_pre, c0, a.d, lane, pre);
+        }
+    }
+    __device__ __forceinline__ void get_post(const ResNormArgs& a, int c0, int lane, float* w) const {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = post[i];
+        } else {
+            read_post(a, c0, lane, w);
+        }
+    }
+    __device__ __forceinline__ void get_pre(const ResNormArgs& a, int c0, int lane, float* w) const {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = pre[i];
+        } else {
+            load8<VEC>(a.w_pre, c0, a.d, lane, w);
+        }
     }
 };
 
-// A row's operands of the forward, as they lie in memory.
-template <typename XT, typename T, bool VEC, bool HAS_Y> struct FwdRow {
-    RawX<XT, VEC> x;
-    Raw8<T, VEC> y, g;
-    __device__ __forceinline__ void load(const ResNormArgs& a, int64_t row, const Place& w) {
-        if (row >= a.n_rows) return;
-        if (HAS_Y) y.load(reinterpret_cast<const T*>(a.y) + row * a.d, w.c0, a.d, w.lane);
-        x.load(a, row, w.c0, w.lane);
-        if (HAS_Y && a.gate_mode == MOM_GATE_ELEMENT)
-            g.load(reinterpret_cast<const T*>(a.gate) + row * a.d, w.c0, a.d, w.lane);
-    }
-};
+// Where the rows' operands come from.  With one chunk a warp a row's operands
+// are held in registers, packed, while it is worked on:
+//   RING    copies in flight to slots in shared memory, two rows ahead (four
+//           without a block's output, when a row is short); each thread reads
+//           only what it copied itself (no barrier), and a slot is filled again
+//           one row after it was read
+//   REGS    loads into registers one row ahead
+//   DIRECT  loads when the row's turn comes, its lines asked into L2 one row
+//           ahead.  Wider rows are read at each use, the later ones from L1.
+enum Source { RING, REGS, DIRECT };
 
-// Rows of the forward ahead of the one at work: copies in flight to a ring of
-// slots in shared memory, of which each thread reads only what it copied (no
-// barrier).  A slot is filled again one row after it was read.  Without a
-// block's output a row is short, so more rows are ahead.  Rows that 16-byte
-// copies cannot take are loaded one ahead into registers.
-template <typename XT, typename T, bool VEC, bool HAS_Y> struct FwdRing {
-    static constexpr int AHEAD = HAS_Y ? 2 : 6, SLOTS = AHEAD + 1;
-    typedef FwdRow<XT, T, VEC, HAS_Y> Row;
-    uint32_t base, pitch, bytes;
+__device__ __forceinline__ void ask_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// HAS_Y: whether there is a block's output (the adjoint asks at run time)
+template <typename XT, typename T, typename G, bool VEC, int C, bool HAS_Y, bool BWD, int SRC> struct Rows {
+    static_assert(C == 1 || SRC == DIRECT, "more than one chunk a warp: no registers to hold a row");
+    static constexpr int SLOTS = HAS_Y ? 3 : 5;
+    typedef RawX<XT, VEC> X;
+    typedef Raw8<T, VEC> Y;
+    typedef Raw8<G, VEC> D;
+    struct Held {
+        X x;
+        Y y, g;
+        D d, h;
+    };
+    const ResNormArgs& a;
+    const ResNormBwdArgs& b;
+    int W, warp, lane;
+    int64_t row, step;
+    Held cur, next;                          // one chunk a warp; REGS: the next row's
+    uint32_t base, pitch, bytes;             // RING
     int in, out;
-    static __host__ __device__ constexpr int pieces(bool elem) {
-        return RawX<XT, true>::R::PIECES + (HAS_Y ? (elem ? 2 : 1) * Raw8<T, true>::PIECES : 0);
+
+    static __host__ __device__ __forceinline__ int pieces(const ResNormArgs& a) {
+        return X::PIECES + (HAS_Y ? (a.gate_mode == MOM_GATE_ELEMENT ? 2 : 1) * Y::PIECES : 0);
     }
-    __device__ __forceinline__ FwdRing(const ResNormArgs& a, void* smem) {
-        pitch = blockDim.x * 16;
-        base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
-        bytes = pieces(a.gate_mode == MOM_GATE_ELEMENT) * pitch;
-        in = out = 0;
+    __device__ __forceinline__ bool has_y() const { return HAS_Y && (!BWD || a.y); }
+    __device__ __forceinline__ int c0(int j) const { return (warp + j * W) * kChunk; }
+    __device__ __forceinline__ const T* at_y(int64_t r) const { return reinterpret_cast<const T*>(a.y) + r * a.d; }
+    __device__ __forceinline__ const T* at_g(int64_t r) const { return reinterpret_cast<const T*>(a.gate) + r * a.d; }
+    __device__ __forceinline__ const G* at_d(int64_t r) const { return reinterpret_cast<const G*>(b.dx_out) + r * a.d; }
+    __device__ __forceinline__ const G* at_h(int64_t r) const { return reinterpret_cast<const G*>(b.dh) + r * a.d; }
+    __device__ __forceinline__ bool elem() const { return HAS_Y && a.gate_mode == MOM_GATE_ELEMENT; }
+
+    __device__ __forceinline__ Rows(const ResNormArgs& a_, const ResNormBwdArgs& b_, void* smem, int W_,
+                                    int warp_, int lane_, int64_t first, int64_t step_)
+        : a(a_), b(b_), W(W_), warp(warp_), lane(lane_), row(first), step(step_) {
+        if constexpr (SRC == RING) {
+            pitch = blockDim.x * 16;
+            base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+            bytes = pieces(a) * pitch;
+            in = out = 0;
+#pragma unroll
+            for (int i = 0; i < SLOTS - 1; ++i) put(row + i * step);
+        } else if constexpr (SRC == REGS) {
+            load(next, first);
+        }
     }
-    __device__ __forceinline__ void put(const ResNormArgs& a, int64_t row, const Place& w) {
-        if (row < a.n_rows) {
+    __device__ __forceinline__ void load(Held& o, int64_t r) {
+        if (r >= a.n_rows) return;
+        if (has_y()) o.y.load(at_y(r), c0(0), a.d, lane);
+        o.x.load(a, r, c0(0), lane);
+        if (elem()) o.g.load(at_g(r), c0(0), a.d, lane);
+        if (BWD && b.dh) o.h.load(at_h(r), c0(0), a.d, lane);
+        if (BWD && b.dx_out) o.d.load(at_d(r), c0(0), a.d, lane);
+    }
+    __device__ __forceinline__ void put(int64_t r) {
+        if (r < a.n_rows) {
             uint32_t at = base + in * bytes;
-            RawX<XT, VEC>::copy(at, pitch, a, row, w.c0, w.lane);
-            at += RawX<XT, VEC>::R::PIECES * pitch;
-            if (HAS_Y) Raw8<T, VEC>::copy(at, pitch, reinterpret_cast<const T*>(a.y) + row * a.d, w.c0, a.d, w.lane);
-            at += Raw8<T, VEC>::PIECES * pitch;
-            if (HAS_Y && a.gate_mode == MOM_GATE_ELEMENT)
-                Raw8<T, VEC>::copy(at, pitch, reinterpret_cast<const T*>(a.gate) + row * a.d, w.c0, a.d, w.lane);
+            X::copy(at, pitch, a, r, c0(0), lane);
+            at += X::PIECES * pitch;
+            if (HAS_Y) Y::copy(at, pitch, at_y(r), c0(0), a.d, lane);
+            at += Y::PIECES * pitch;
+            if (elem()) Y::copy(at, pitch, at_g(r), c0(0), a.d, lane);
         }
         in = in + 1 == SLOTS ? 0 : in + 1;
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    __device__ __forceinline__ void take(const ResNormArgs& a, Row& r) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+    __device__ __forceinline__ void take() {
+        asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 2) : "memory");      // all but the youngest
         uint32_t at = base + out * bytes;
-        r.x.r.take(at, pitch);
-        at += RawX<XT, VEC>::R::PIECES * pitch;
-        if (HAS_Y) r.y.take(at, pitch);
-        at += Raw8<T, VEC>::PIECES * pitch;
-        if (HAS_Y && a.gate_mode == MOM_GATE_ELEMENT) r.g.take(at, pitch);
+        cur.x.take(at, pitch);
+        at += X::PIECES * pitch;
+        if (HAS_Y) cur.y.take(at, pitch);
+        at += Y::PIECES * pitch;
+        if (elem()) cur.g.take(at, pitch);
         out = out + 1 == SLOTS ? 0 : out + 1;
     }
-};
-template <typename XT, typename T, bool HAS_Y> struct FwdRing<XT, T, false, HAS_Y> {
-    typedef FwdRow<XT, T, false, HAS_Y> Row;
-    static constexpr int AHEAD = 1, SLOTS = 0;
-    Row next;
-    static constexpr int pieces(bool) { return 0; }
-    __device__ __forceinline__ FwdRing(const ResNormArgs&, void*) {}
-    __device__ __forceinline__ void put(const ResNormArgs& a, int64_t row, const Place& w) { next.load(a, row, w); }
-    __device__ __forceinline__ void take(const ResNormArgs&, Row& r) { r = next; }
+    __device__ __forceinline__ void ask(int64_t r) const {
+        if (r >= a.n_rows) return;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const int c = c0(j) + lane * 8;
+            if (c >= a.d) continue;
+            if (a.x) ask_l2(reinterpret_cast<const char*>(a.x) + (r * a.d + c) * (std::is_same<XT, bf16>::value ? 2 : 4));
+            else ask_l2(a.x_codes + r * a.d + c);
+            if (has_y()) ask_l2(at_y(r) + c);
+            if (elem()) ask_l2(at_g(r) + c);
+            if (BWD && b.dh) ask_l2(at_h(r) + c);
+            if (BWD && b.dx_out) ask_l2(at_d(r) + c);
+        }
+    }
+    // the row at work is there, and a later one is on its way
+    __device__ __forceinline__ void begin() {
+        if constexpr (SRC == RING) {
+            take();
+            put(row + (SLOTS - 1) * step);
+        } else if constexpr (SRC == REGS) {
+            cur = next;
+            load(next, row + step);
+        } else {
+            if constexpr (C == 1) load(cur, row);
+            ask(row + step);
+        }
+    }
+    __device__ __forceinline__ void x(int j, X& o) const {
+        if constexpr (C == 1) o = cur.x;
+        else o.load(a, row, c0(j), lane);
+    }
+    __device__ __forceinline__ void y(int j, float* v) const {
+        if constexpr (C == 1) { cur.y.get(v); return; }
+        Y o;
+        o.load(at_y(row), c0(j), a.d, lane);
+        o.get(v);
+    }
+    __device__ __forceinline__ void g(int j, float* v) const {
+        if constexpr (C == 1) { cur.g.get(v); return; }
+        Y o;
+        o.load(at_g(row), c0(j), a.d, lane);
+        o.get(v);
+    }
+    __device__ __forceinline__ void h(int j, float* v) const {
+        if constexpr (C == 1) { cur.h.get(v); return; }
+        D o;
+        o.load(at_h(row), c0(j), a.d, lane);
+        o.get(v);
+    }
+    __device__ __forceinline__ void d(int j, float* v) const {
+        if constexpr (C == 1) { cur.d.get(v); return; }
+        D o;
+        o.load(at_d(row), c0(j), a.d, lane);
+        o.get(v);
+    }
 };
 
-// CTAs (clusters; warps, with one warp a row) walk the rows.  `red` alternates
-// between two rows, so that one barrier a sum is enough.
-template <typename XT, typename T, bool VEC, bool HAS_Y>
-__global__ void __launch_bounds__(32 * kWarps, VEC ? 3 : 2) residual_norm_kernel(const ResNormArgs a) {
-    extern __shared__ __align__(16) unsigned char slots[];
-    __shared__ float red[2][2][kMaxCluster * kWarps];
-    typedef FwdRing<XT, T, VEC, HAS_Y> Ring;
-    const Place w(a);
-    const int rows_cta = w.W > 1 ? 1 : blockDim.x >> 5;
-    const int64_t step = (int64_t)gridDim.x / w.cl * rows_cta;
-    int64_t row = (int64_t)(blockIdx.x / w.cl) * rows_cta + (w.W > 1 ? 0 : threadIdx.x >> 5);
+// CTAs (warps, with one warp a row) walk the rows.  `red` alternates between
+// two rows, so that one barrier a sum is enough.
+template <typename XT, typename T, bool VEC, int C, bool HAS_Y, int SRC, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : SRC != RING ? 2 : HAS_Y ? 3 : 4)
+residual_norm_kernel(const ResNormArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float red[2][2][kMaxWarps];
+    const int lane = threadIdx.x & 31, W = a.warps_per_row, warp = W > 1 ? threadIdx.x >> 5 : 0;
+    const int rows_cta = W > 1 ? 1 : blockDim.x >> 5;
+    const int64_t step = (int64_t)gridDim.x * rows_cta;
+    const int64_t first = (int64_t)blockIdx.x * rows_cta + (W > 1 ? 0 : threadIdx.x >> 5);
     const int d = a.d;
     const float inv_d = 1.f / (float)d;
-    Ring ring(a, slots);
-#pragma unroll
-    for (int i = 0; i < Ring::AHEAD; ++i) ring.put(a, row + i * step, w);
+    const ResNormBwdArgs none{};
+    Rows<XT, T, T, VEC, C, HAS_Y, false, SRC> in(a, none, smem, W, warp, lane, first, step);
     T gate_next = from_f<T>(0.f);
-    if (a.gate_mode == MOM_GATE_TOKEN && row < a.n_rows) gate_next = reinterpret_cast<const T*>(a.gate)[row];
-    const Weights<VEC> wt(a, a.h != nullptr, w);
-    if (w.cl > 1) cluster_barrier();          // the other CTAs' shared memory is there
-    for (int buf = 0; row < a.n_rows; row += step, buf ^= 1) {      // the same count in all warps of a row
-        FwdRow<XT, T, VEC, HAS_Y> r;
-        ring.take(a, r);
-        ring.put(a, row + Ring::AHEAD * step, w);
+    if (a.gate_mode == MOM_GATE_TOKEN && first < a.n_rows) gate_next = reinterpret_cast<const T*>(a.gate)[first];
+    const Weights<VEC, C> wt(a, a.h != nullptr, warp * kChunk, lane);
+    for (int buf = 0; in.row < a.n_rows; in.row += in.step, buf ^= 1) {      // the same count in all warps of a row
+        const int64_t row = in.row;
+        in.begin();
         const T gate = gate_next;
         if (a.gate_mode == MOM_GATE_TOKEN && row + step < a.n_rows)
             gate_next = reinterpret_cast<const T*>(a.gate)[row + step];
-        float xv[8], ry = 0.f;
+        float xv[C][8], ry = 0.f, ss[1] = {0.f};
         if (HAS_Y) {
-            float ss[1] = {0.f}, y[8];
-            r.y.get(y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss[0] = fmaf(y[i], y[i], ss[0]);
-            row_sum<1>(ss, red[buf][0], w);
+            for (int j = 0; j < C; ++j) {
+                float y[8];
+                in.y(j, y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss[0] = fmaf(y[i], y[i], ss[0]);
+            }
+            row_sum<1>(ss, red[buf][0], W, warp, lane);
             ry = rsqrtf(ss[0] * inv_d + a.eps);                     // 1 / rms(y), times a token's gate
             if (a.gate_mode == MOM_GATE_TOKEN) ry *= sigmoid(to_f(gate));
         }
-        r.x.get(xv);
-        if constexpr (!std::is_same<XT, Q8>::value) {
-            if (a.codes_out) {
-                uint32_t m[2];
-                r.x.r.amax(m);
-                act8_store<VEC>(xv, m, w.c0, d, w.lane, a.codes_out + row * d, a.scales_out + row * a.groups);
+        ss[0] = 0.f;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const int c0 = in.c0(j);
+            RawX<XT, VEC> x;
+            in.x(j, x);
+            x.get(xv[j]);
+            if constexpr (!std::is_same<XT, Q8>::value) {
+                if (a.codes_out) {
+                    uint32_t m[2];
+                    x.amax(m);
+                    act8_store<VEC>(xv[j], m, c0, d, lane, a.codes_out + row * d, a.scales_out + row * a.groups);
+                }
             }
-        }
-        if (HAS_Y) {
-            float y[8];
-            r.y.get(y);
+            if (HAS_Y) {
+                float y[8], w[8];
+                in.y(j, y);
+                wt.get_post(a, c0, lane, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] *= ry;
-            if (a.gate_mode == MOM_GATE_ELEMENT) {
-                float g[8];
-                r.g.get(g);
+                for (int i = 0; i < 8; ++i) y[i] *= ry;
+                if (a.gate_mode == MOM_GATE_ELEMENT) {
+                    float g[8];
+                    in.g(j, g);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] *= sigmoid(g[i]);
+                    for (int i = 0; i < 8; ++i) y[i] *= sigmoid(g[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) xv[j][i] = fmaf(y[i], w[i], xv[j][i]);
+            }
+            if (a.x_out) {
+                if (a.x_out_f32) store8<VEC>(reinterpret_cast<float*>(a.x_out) + row * d, c0, d, lane, xv[j]);
+                else store8<VEC>(reinterpret_cast<bf16*>(a.x_out) + row * d, c0, d, lane, xv[j]);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) xv[i] = fmaf(y[i], wt.post[i], xv[i]);
-        }
-        if (a.x_out) {
-            if (a.x_out_f32) store8<VEC>(reinterpret_cast<float*>(a.x_out) + row * d, w.c0, d, w.lane, xv);
-            else store8<VEC>(reinterpret_cast<bf16*>(a.x_out) + row * d, w.c0, d, w.lane, xv);
+            for (int i = 0; i < 8; ++i) ss[0] = fmaf(xv[j][i], xv[j][i], ss[0]);
         }
         if (a.h) {
-            float ss[1] = {0.f};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss[0] = fmaf(xv[i], xv[i], ss[0]);
-            row_sum<1>(ss, red[buf][1], w);
+            row_sum<1>(ss, red[buf][1], W, warp, lane);
             const float rx = rsqrtf(ss[0] * inv_d + a.eps);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) xv[i] *= rx * wt.pre[i];
-            store8<VEC>(reinterpret_cast<T*>(a.h) + row * d, w.c0, d, w.lane, xv);
+            for (int j = 0; j < C; ++j) {
+                float w[8];
+                wt.get_pre(a, in.c0(j), lane, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) xv[j][i] *= rx * w[i];
+                store8<VEC>(reinterpret_cast<T*>(a.h) + row * d, in.c0(j), d, lane, xv[j]);
+            }
         }
     }
 }
 
-// A row's operands of the adjoint, as they lie in memory.
-template <typename XT, typename T, typename G, bool VEC> struct BwdRow {
-    RawX<XT, VEC> x;
-    Raw8<T, VEC> y, g;
-    Raw8<G, VEC> d, h;
-    T gate;
-    __device__ __forceinline__ void load(const ResNormArgs& a, const ResNormBwdArgs& b, int64_t row, const Place& w) {
-        if (row >= a.n_rows) return;
-        const int n = a.d;
-        if (a.y) y.load(reinterpret_cast<const T*>(a.y) + row * n, w.c0, n, w.lane);
-        x.load(a, row, w.c0, w.lane);
-        if (a.gate_mode == MOM_GATE_ELEMENT) g.load(reinterpret_cast<const T*>(a.gate) + row * n, w.c0, n, w.lane);
-        if (b.dh) h.load(reinterpret_cast<const G*>(b.dh) + row * n, w.c0, n, w.lane);
-        if (b.dx_out) d.load(reinterpret_cast<const G*>(b.dx_out) + row * n, w.c0, n, w.lane);
-        if (a.gate_mode == MOM_GATE_TOKEN) gate = reinterpret_cast<const T*>(a.gate)[row];
-    }
-};
-
-// The adjoint.  CTAs (clusters) walk the rows; the next row's operands are
-// loaded (packed) before this row's arithmetic, so that loads are in flight
-// through its three reductions.  Threads keep the two column sums (A and
-// dw_pre) of their channels in registers and write them once as a partial,
-// which cols_reduce_kernel adds up in order: no atomics, the same sums every
-// time on the same device.
-template <typename XT, typename T, typename G, bool VEC>
-__global__ void __launch_bounds__(32 * kWarps, 2) residual_norm_bwd_kernel(const ResNormArgs a,
-                                                                           const ResNormBwdArgs b) {
-    __shared__ float red[2][4][kMaxCluster * kWarps];
-    const Place w(a);
+// The adjoint.  Threads keep the two column sums (A and dw_pre) of their
+// channels in registers over all of a CTA's rows and write them once as a
+// partial, which cols_reduce_kernel adds up in CTA order: no atomics, the same
+// sums every time on the same device.  With one chunk a warp n_y and sigma stay
+// in registers between the passes over a row, else they are formed again.
+template <typename XT, typename T, typename G, bool VEC, int C, int SRC, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : 2)
+residual_norm_bwd_kernel(const ResNormArgs a, const ResNormBwdArgs b) {
+    __shared__ float red[2][4][kMaxWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     const int d = a.d;
-    const int64_t step = gridDim.x / w.cl, first = blockIdx.x / w.cl;
     const float inv_d = 1.f / (float)d;
-    float accA[8], accP[8];
+    float accA[C][8], accP[C][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) accA[i] = accP[i] = 0.f;
-    BwdRow<XT, T, G, VEC> next;
-    next.load(a, b, first, w);
-    const Weights<VEC> wt(a, b.dh != nullptr, w);
-    if (w.cl > 1) cluster_barrier();          // the other CTAs' shared memory is there
-    int buf = 0;
-    for (int64_t row = first; row < a.n_rows; row += step, buf ^= 1) {
-        const BwdRow<XT, T, G, VEC> r = next;
-        next.load(a, b, row + step, w);
-        float yv[8], gv[8], dv[8];
+    for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) accA[j][i] = accP[j][i] = 0.f;
+    Rows<XT, T, G, VEC, C, true, true, SRC> in(a, b, nullptr, W, warp, lane, blockIdx.x, gridDim.x);
+    T gate_next = from_f<T>(0.f);
+    if (a.gate_mode == MOM_GATE_TOKEN && in.row < a.n_rows) gate_next = reinterpret_cast<const T*>(a.gate)[in.row];
+    const Weights<VEC, C> wt(a, b.dh != nullptr, warp * kChunk, lane);
+    for (int buf = 0; in.row < a.n_rows; in.row += in.step, buf ^= 1) {
+        const int64_t row = in.row;
+        in.begin();
+        const T gate = gate_next;
+        if (a.gate_mode == MOM_GATE_TOKEN && row + in.step < a.n_rows)
+            gate_next = reinterpret_cast<const T*>(a.gate)[row + in.step];
+        float yk[C == 1 ? 8 : 1], gk[C == 1 ? 8 : 1], dv[C][8];
         float gt = 1.f, rest = 0.f, ry = 0.f;
-        if (a.gate_mode == MOM_GATE_TOKEN) gt = sigmoid(to_f(r.gate), rest);
-        if (a.y) {
-            float ss[1] = {0.f};
-            r.y.get(yv);
+        if (a.gate_mode == MOM_GATE_TOKEN) gt = sigmoid(to_f(gate), rest);
+        // n_y and sigma of chunk j
+        auto form = [&](int j, float* y, float* g) {
+            in.y(j, y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss[0] = fmaf(yv[i], yv[i], ss[0]);
-            row_sum<1>(ss, red[buf][0], w);
-            ry = rsqrtf(ss[0] * inv_d + a.eps);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) yv[i] *= ry;                          // n_y
+            for (int i = 0; i < 8; ++i) y[i] *= ry;
             if (a.gate_mode == MOM_GATE_ELEMENT) {
-                r.g.get(gv);
+                in.g(j, g);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) gv[i] = sigmoid(gv[i]);
+                for (int i = 0; i < 8; ++i) g[i] = sigmoid(g[i]);
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) gv[i] = gt;
+                for (int i = 0; i < 8; ++i) g[i] = gt;
             }
-        }
-        if (b.dx_out) {
-            r.d.get(dv);
-        } else {
+        };
+        auto again = [&](int j, float* y, float* g) {
+            if constexpr (C == 1) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dv[i] = 0.f;
+                for (int i = 0; i < 8; ++i) { y[i] = yk[i]; g[i] = gk[i]; }
+            } else {
+                form(j, y, g);
+            }
+        };
+        if (a.y) {
+            float ss[1] = {0.f};
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                float y[8];
+                in.y(j, y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss[0] = fmaf(y[i], y[i], ss[0]);
+            }
+            row_sum<1>(ss, red[buf][0], W, warp, lane);
+            ry = rsqrtf(ss[0] * inv_d + a.eps);
+            if constexpr (C == 1) form(0, yk, gk);
         }
         if (b.dh) {
-            float ss[2] = {0.f, 0.f}, xv[8], hv[8];
-            r.x.get(xv);
-            r.h.get(hv);
-            if (a.y) {
+            float ss[2] = {0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) xv[i] = fmaf(yv[i] * gv[i], wt.post[i], xv[i]);      // x'
-            }
+            for (int j = 0; j < C; ++j) {                                     // dv: x' for now
+                float h[8], w[8];
+                RawX<XT, VEC> x;
+                in.x(j, x);
+                x.get(dv[j]);
+                if (a.y) {
+                    float y[8], g[8];
+                    again(j, y, g);
+                    wt.get_post(a, in.c0(j), lane, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                ss[0] = fmaf(xv[i], xv[i], ss[0]);
-                ss[1] = fmaf(xv[i], hv[i] * wt.pre[i], ss[1]);
+                    for (int i = 0; i < 8; ++i) dv[j][i] = fmaf(y[i] * g[i], w[i], dv[j][i]);
+                }
+                in.h(j, h);
+                wt.get_pre(a, in.c0(j), lane, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    ss[0] = fmaf(dv[j][i], dv[j][i], ss[0]);
+                    ss[1] = fmaf(dv[j][i], h[i] * w[i], ss[1]);
+                }
             }
-            row_sum<2>(ss, red[buf][1], w);
+            row_sum<2>(ss, red[buf][1], W, warp, lane);
             const float rx = rsqrtf(ss[0] * inv_d + a.eps);
             const float k = ss[1] * inv_d * rx * rx * rx;                     // mean(dn n_x) / rms / rms
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float hr = hv[i] * rx;
-                accP[i] = fmaf(hr, xv[i], accP[i]);
-                dv[i] = fmaf(hr, wt.pre[i], fmaf(xv[i], -k, dv[i]));
-            }
-        }
-        store8<VEC>(reinterpret_cast<G*>(b.dx) + row * d, w.c0, d, w.lane, dv);
-        if (a.y) {
-            float ss[1] = {0.f}, o[8];
+            for (int j = 0; j < C; ++j) {
+                float h[8], w[8], o[8];
+                in.h(j, h);
+                wt.get_pre(a, in.c0(j), lane, w);
+                if (b.dx_out) {
+                    in.d(j, o);
+                } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float t = dv[i] * gv[i];
-                accA[i] = fmaf(t, yv[i], accA[i]);
-                dv[i] = t * wt.post[i];                                       // u = D s sigma w_post
-                ss[0] = fmaf(dv[i], yv[i], ss[0]);
-            }
-            row_sum<1>(ss, red[buf][3], w);
-            const float m = ss[0] * inv_d * ry;
-            if (a.gate_mode == MOM_GATE_TOKEN && b.dgate && threadIdx.x == 0 && w.rank == 0)
-                reinterpret_cast<T*>(b.dgate)[row] = from_f<T>(ss[0] * rest);
-            if (a.gate_mode == MOM_GATE_ELEMENT && b.dgate) {
-                r.g.get(o);
+                    for (int i = 0; i < 8; ++i) o[i] = 0.f;
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    float q;
-                    sigmoid(o[i], q);
-                    o[i] = dv[i] * yv[i] * q;
+                    const float hr = h[i] * rx;
+                    accP[j][i] = fmaf(hr, dv[j][i], accP[j][i]);
+                    dv[j][i] = fmaf(hr, w[i], fmaf(dv[j][i], -k, o[i]));      // D
                 }
-                store8<VEC>(reinterpret_cast<T*>(b.dgate) + row * d, w.c0, d, w.lane, o);
             }
+        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = fmaf(dv[i], ry, -yv[i] * m);
-            store8<VEC>(reinterpret_cast<T*>(b.dy) + row * d, w.c0, d, w.lane, o);
+            for (int j = 0; j < C; ++j) in.d(j, dv[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < C; ++j) store8<VEC>(reinterpret_cast<G*>(b.dx) + row * d, in.c0(j), d, lane, dv[j]);
+        if (a.y) {
+            float ss[1] = {0.f};
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                float y[8], g[8], w[8];
+                again(j, y, g);
+                wt.get_post(a, in.c0(j), lane, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float t = dv[j][i] * g[i];
+                    accA[j][i] = fmaf(t, y[i], accA[j][i]);
+                    dv[j][i] = t * w[i];                                      // u = D s sigma w_post
+                    ss[0] = fmaf(dv[j][i], y[i], ss[0]);
+                }
+            }
+            row_sum<1>(ss, red[buf][3], W, warp, lane);
+            const float m = ss[0] * inv_d * ry;
+            if (a.gate_mode == MOM_GATE_TOKEN && b.dgate && threadIdx.x == 0)
+                reinterpret_cast<T*>(b.dgate)[row] = from_f<T>(ss[0] * rest);
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                float y[8], o[8];
+                if constexpr (C == 1) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = yk[i];
+                } else {
+                    in.y(j, y);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] *= ry;
+                }
+                if (a.gate_mode == MOM_GATE_ELEMENT && b.dgate) {
+                    in.g(j, o);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float q;
+                        sigmoid(o[i], q);
+                        o[i] = dv[j][i] * y[i] * q;
+                    }
+                    // dy may be y and dgate the gate: this thread's own elements, read before
+                    store8<VEC>(reinterpret_cast<T*>(b.dgate) + row * d, in.c0(j), d, lane, o);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = fmaf(dv[j][i], ry, -y[i] * m);
+                store8<VEC>(reinterpret_cast<T*>(b.dy) + row * d, in.c0(j), d, lane, o);
+            }
         }
     }
-    float* pa = b.partial + first * 2 * d;
-    store8<VEC>(pa, w.c0, d, w.lane, accA);
-    store8<VEC>(pa + d, w.c0, d, w.lane, accP);
+    float* pa = b.partial + (int64_t)blockIdx.x * 2 * d;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        store8<VEC>(pa, in.c0(j), d, lane, accA[j]);
+        store8<VEC>(pa + d, in.c0(j), d, lane, accP[j]);
+    }
 }
 
 // Column sums of the CTAs' partials: a CTA sums 32 channels of one of the two
@@ -429,84 +552,82 @@ int sm_count() {
     return sms;
 }
 
-// CTAs of a row's cluster and warps of a CTA.
+// Chunks a warp and warps of a row.
 struct Shape {
-    int cluster, warps;
+    int C, warps;
 };
 Shape shape_for(int d) {
-    const int chunks = (int)cdiv(d, kChunk);
-    int cl = 1;
-    while (cl * kWarps < chunks) cl *= 2;
-    return {cl, (int)cdiv(chunks, cl)};
+    const int chunks = (int)cdiv(d, kChunk), C = chunks <= 16 ? 1 : chunks <= 32 ? 2 : 4;
+    return {C, (int)cdiv(chunks, C)};
 }
 
-template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), int64_t ctas, int threads, size_t smem, int cluster, cudaStream_t st,
-                   const A&... args) {
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = cluster;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = &at;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-// Warps an SM that the registers leave (__launch_bounds__).
-constexpr int kFwdWarps = 24, kWarpsSM = 16;
+// Warps an SM that the registers leave (__launch_bounds__): the forward's ring
+// with up to 8 warps a row needs 80 registers, 64 without a block's output,
+// everything else 128.
+constexpr int kRingWarps = 24, kShortWarps = 32, kWarps = 16;
 constexpr int kSmemSM = 220 * 1024;
 
-template <typename XT, typename T, bool VEC, bool HAS_Y> cudaError_t run_fwd(ResNormArgs a, cudaStream_t st) {
-    typedef FwdRing<XT, T, VEC, HAS_Y> Ring;
-    auto* kernel = residual_norm_kernel<XT, T, VEC, HAS_Y>;
-    const Shape s = shape_for(a.d);
-    a.cluster = s.cluster;
-    a.warps_per_row = s.warps;
-    const bool own = s.warps * s.cluster == 1;                 // a row a warp
-    const int threads = own ? 128 : 32 * s.warps;
-    const size_t smem = (size_t)Ring::SLOTS * Ring::pieces(a.gate_mode == MOM_GATE_ELEMENT) * threads * 16;
-    static unsigned long long optin_done = 0;
-    const cudaError_t e = smem_optin((const void*)kernel, Ring::SLOTS * Ring::pieces(true) * 32 * kWarps * 16, &optin_done);
-    if (e != cudaSuccess) return e;
-    int ctas = (VEC ? kFwdWarps : kWarpsSM) / (threads / 32);
-    if (smem * ctas > kSmemSM) ctas = (int)(kSmemSM / smem);
-    const int64_t units = own ? cdiv(a.n_rows, threads / 32) : a.n_rows;
-    const int64_t most = (int64_t)sm_count() * ctas / s.cluster;
-    return launch(kernel, (units < most ? units : most) * s.cluster, threads, smem, s.cluster, st, a);
+template <typename XT, typename T, bool VEC, int C, bool HAS_Y, int MAXT>
+cudaError_t run_fwd(ResNormArgs a, cudaStream_t st) {
+    constexpr int SRC = C > 1 ? DIRECT : VEC ? RING : REGS;
+    auto* kernel = residual_norm_kernel<XT, T, VEC, C, HAS_Y, SRC, MAXT>;
+    const int W = shape_for(a.d).warps, threads = W == 1 ? 128 : 32 * W;
+    a.warps_per_row = W;
+    const int ctas = (SRC != RING || MAXT > 256 ? kWarps : HAS_Y ? kRingWarps : kShortWarps) / (threads / 32);
+    size_t smem = 0;
+    if (SRC == RING) {
+        typedef Rows<XT, T, T, VEC, C, HAS_Y, false, SRC> R;
+        // at most 24 warps x 6 pieces x 3 slots: 216 KB an SM
+        smem = (size_t)R::SLOTS * R::pieces(a) * threads * 16;
+        static unsigned long long optin_done = 0;
+        const cudaError_t e = smem_optin((const void*)kernel, kSmemSM, &optin_done);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t units = W == 1 ? cdiv(a.n_rows, threads / 32) : a.n_rows, most = (int64_t)sm_count() * ctas;
+    kernel<<<(unsigned)(units < most ? units : most), threads, smem, st>>>(a);
+    return cudaGetLastError();
 }
 
-template <typename XT, typename T, typename G, bool VEC>
+template <typename XT, typename T, typename G, bool VEC, int C, int MAXT>
 cudaError_t run_bwd(ResNormArgs a, const ResNormBwdArgs& b, int parts, cudaStream_t st) {
+    constexpr int SRC = C > 1 || !VEC ? DIRECT : REGS;
+    a.warps_per_row = shape_for(a.d).warps;
+    residual_norm_bwd_kernel<XT, T, G, VEC, C, SRC, MAXT><<<parts, 32 * a.warps_per_row, 0, st>>>(a, b);
+    return cudaGetLastError();
+}
+
+template <typename XT, typename T, bool VEC, bool HAS_Y> cudaError_t shape_fwd(const ResNormArgs& a, cudaStream_t st) {
     const Shape s = shape_for(a.d);
-    a.cluster = s.cluster;
-    a.warps_per_row = s.warps;
-    return launch(residual_norm_bwd_kernel<XT, T, G, VEC>, (int64_t)parts * s.cluster, 32 * s.warps, 0, s.cluster, st, a, b);
+    if (s.C == 1) return s.warps <= 8 ? run_fwd<XT, T, VEC, 1, HAS_Y, 256>(a, st) : run_fwd<XT, T, VEC, 1, HAS_Y, 512>(a, st);
+    return s.C == 2 ? run_fwd<XT, T, VEC, 2, HAS_Y, 512>(a, st) : run_fwd<XT, T, VEC, 4, HAS_Y, 512>(a, st);
+}
+template <typename XT, typename T, bool VEC> cudaError_t pick_fwd(const ResNormArgs& a, cudaStream_t st) {
+    return a.y ? shape_fwd<XT, T, VEC, true>(a, st) : shape_fwd<XT, T, VEC, false>(a, st);
+}
+template <typename XT, typename T, typename G, bool VEC>
+cudaError_t pick_bwd(const ResNormArgs& a, const ResNormBwdArgs& b, int parts, cudaStream_t st) {
+    const Shape s = shape_for(a.d);
+    if (s.C == 1) return s.warps <= 8 ? run_bwd<XT, T, G, VEC, 1, 256>(a, b, parts, st) : run_bwd<XT, T, G, VEC, 1, 512>(a, b, parts, st);
+    return s.C == 2 ? run_bwd<XT, T, G, VEC, 2, 512>(a, b, parts, st) : run_bwd<XT, T, G, VEC, 4, 512>(a, b, parts, st);
 }
 
 }  // namespace
 
 // rows of partial column sums the adjoint writes
 int residual_norm_bwd_parts(int64_t n_rows, int d) {
-    const Shape s = shape_for(d);
-    const int64_t most = (int64_t)sm_count() * (kWarpsSM / s.warps) / s.cluster;
+    const int64_t most = (int64_t)sm_count() * (kWarps / shape_for(d).warps);
     return (int)(n_rows < most ? n_rows : most);
 }
 
 cudaError_t launch_residual_norm(const ResNormArgs& a, int x_kind, int dt, bool vec, cudaStream_t st) {
     cudaError_t e;
-#define MOM_RN(XT, T) e = a.y ? (vec ? run_fwd<XT, T, true, true>(a, st) : run_fwd<XT, T, false, true>(a, st)) \
-                        : (vec ? run_fwd<XT, T, true, false>(a, st) : run_fwd<XT, T, false, false>(a, st))
+#define MOM_RN(XT, T) e = vec ? pick_fwd<XT, T, true>(a, st) : pick_fwd<XT, T, false>(a, st)
     if (x_kind == RN_X_BF16) MOM_RN(bf16, bf16);
     else if (x_kind == RN_X_F32) { if (dt == MOM_BF16) MOM_RN(float, bf16); else MOM_RN(float, float); }
     else { if (dt == MOM_BF16) MOM_RN(Q8, bf16); else MOM_RN(Q8, float); }
 #undef MOM_RN
     count_launches(1);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_residual_norm_bwd(const ResNormArgs& a, const ResNormBwdArgs& b, int x_kind, int dt, int g_dt,
@@ -514,7 +635,7 @@ cudaError_t launch_residual_norm_bwd(const ResNormArgs& a, const ResNormBwdArgs&
     const int parts = residual_norm_bwd_parts(a.n_rows, a.d);
     if (parts > 0) {
         cudaError_t e;
-#define MOM_RNB(XT, T, G) e = vec ? run_bwd<XT, T, G, true>(a, b, parts, st) : run_bwd<XT, T, G, false>(a, b, parts, st)
+#define MOM_RNB(XT, T, G) e = vec ? pick_bwd<XT, T, G, true>(a, b, parts, st) : pick_bwd<XT, T, G, false>(a, b, parts, st)
 #define MOM_RNG(XT, T) do { if (g_dt == MOM_BF16) { MOM_RNB(XT, T, bf16); } else { MOM_RNB(XT, T, float); } } while (0)
         if (x_kind == RN_X_BF16) MOM_RNG(bf16, bf16);
         else if (x_kind == RN_X_F32) { if (dt == MOM_BF16) MOM_RNG(float, bf16); else MOM_RNG(float, float); }

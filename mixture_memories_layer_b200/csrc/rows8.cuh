@@ -44,6 +44,7 @@ __device__ __forceinline__ float fast_ex2(float x) {
 // in flight.  With VEC, d is a multiple of 8 and a lane's 8 channels are all in
 // or all out.
 template <typename T, bool VEC> struct Raw8 {
+    static constexpr int PIECES = 0;
     float v[8];
     __device__ __forceinline__ void load(const T* row, int c0, int d, int lane) {
 #pragma unroll
@@ -270,6 +271,7 @@ template <> struct Raw8Q<true> {
     }
 };
 template <> struct Raw8Q<false> {
+    static constexpr int PIECES = 0;
     float v[8];
     __device__ __forceinline__ void load(const int8_t* codes_row, const float* scales_row, int c0, int d, int lane) {
         const int g0 = c0 / kActGroup;

@@ -629,29 +629,55 @@ MOM_ACT8_GROUP, MOM_NORM_MAX_D = 128, 16384
 MOM_GATE_NONE, MOM_GATE_TOKEN, MOM_GATE_ELEMENT = 0, 1, 2
 
 
-def _want(name, t, shape, dtypes, like):
-    """The library reads and writes as many elements as the sizes say: a tensor
-    of another shape, type or device is refused here."""
-    if t is None:
-        return
+def _refuse(name, t, shape, dtype, dev):
     if tuple(t.shape) != tuple(shape):
         raise ValueError("MoM: %s has shape %s, %s is wanted" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype not in dtypes:
-        raise ValueError("MoM: %s is %s, %s is wanted" % (name, t.dtype, " or ".join(str(d) for d in dtypes)))
-    if t.device != like.device:
-        raise ValueError("MoM: %s is on %s, not on %s" % (name, t.device, like.device))
+    if t.dtype != dtype:
+        raise ValueError("MoM: %s is %s, %s is wanted" % (name, t.dtype, dtype))
+    if t.get_device() != dev:
+        raise ValueError("MoM: %s is on %s, not on the first operand's device" % (name, t.device))
+    raise ValueError("MoM: %s is not contiguous (shape %s, strides %s); use .contiguous()"
+                     % (name, tuple(t.shape), t.stride()))
 
 
-def _run(what, like, stream, fn, *args):
-    """fn(*args, stream) on the device of ``like``."""
-    if like.is_cuda and like.device.index != torch.cuda.current_device():
-        with torch.cuda.device(like.device):
-            _check(fn(*args, _s(stream)), what)
+def _arg(name, t, shape, dtype, dev):
+    """Device pointer of an operand (None -> NULL).  The library reads and
+    writes as many elements as the sizes say: a tensor of another shape, type
+    or device, or a strided view, is refused here."""
+    if t is None:
+        return None
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(name, t, shape, dtype, dev)
+
+
+def _arg_ws(ws, dev):
+    if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("MoM: the workspace is %s on %s, contiguous uint8 on the operands' device is wanted"
+                         % (ws.dtype, ws.device))
+    return ws.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _launch(what, fn, dev, stream, *args):
+    """fn(*args, stream) on device `dev`; stream None: that device's current one."""
+    if dev < 0:
+        raise ValueError("MoM: %s was given host tensors; the library takes CUDA tensors" % what)
+    st = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if _current_device() == dev:
+        status = fn(*args, st)
     else:
-        _check(fn(*args, _s(stream)), what)
+        with torch.cuda.device(dev):
+            status = fn(*args, st)
+    if status != MOM_OK:
+        _check(status, what)
 
 
-_F32, _ANY = (torch.float32,), (torch.float32, torch.bfloat16)
+_F32, _BF16, _I8 = torch.float32, torch.bfloat16, torch.int8
 
 
 def new_act8(n_rows, d, device=None):
@@ -662,51 +688,53 @@ def new_act8(n_rows, d, device=None):
             torch.empty((n_rows, -(-d // MOM_ACT8_GROUP)), dtype=torch.float32, device=dev))
 
 
-def _want_act8(k8, n, d, like):
+def _arg_act8(k8, n, d, dev):
     codes, scales = k8
-    _want("codes", codes, (n, d), (torch.int8,), like)
-    _want("scales", scales, (n, -(-d // MOM_ACT8_GROUP)), _F32, like)
-    return codes, scales
+    return (_arg("codes", codes, (n, d), _I8, dev),
+            _arg("scales", scales, (n, -(-d // MOM_ACT8_GROUP)), _F32, dev))
 
 
 def mom_act_pack8(x, k8, stream=None):
     """x [n, d] -> the 8-bit checkpoint k8 = (codes, scales) (new_act8)."""
     n, d = x.shape
-    codes, scales = _want_act8(k8, n, d, x)
-    _run("mom_act_pack8", x, stream, lib.mom_act_pack8, _p(x), dtype_code(x.dtype), n, d, _p(codes), _p(scales))
+    dev, dt = x.get_device(), x.dtype
+    codes, scales = _arg_act8(k8, n, d, dev)
+    _launch("mom_act_pack8", lib.mom_act_pack8, dev, stream, _arg("x", x, (n, d), dt, dev), dtype_code(dt), n, d, codes,
+            scales)
 
 
 def mom_act_unpack8(k8, x, stream=None):
     """The restored values of the checkpoint k8 into x [n, d]."""
     n, d = x.shape
-    codes, scales = _want_act8(k8, n, d, x)
-    _run("mom_act_unpack8", x, stream, lib.mom_act_unpack8, _p(codes), _p(scales), n, d, _p(x), dtype_code(x.dtype))
+    dev, dt = x.get_device(), x.dtype
+    codes, scales = _arg_act8(k8, n, d, dev)
+    _launch("mom_act_unpack8", lib.mom_act_unpack8, dev, stream, codes, scales, n, d, _arg("x", x, (n, d), dt, dev),
+            dtype_code(dt))
 
 
-def _res_norm(x, y, gate, w_post, res_scale, w_pre, x_dt, dt):
-    """(x, codes, scales, gate mode, n, d) of the residual norm's calls, its
-    operands' shapes checked."""
-    codes = scales = None
+def _arg_norm(x, y, gate, w_post, res_scale, w_pre, x_dt, dt):
+    """The operands that the residual norm and its adjoint share, checked:
+    (device, n, d, the C arguments from x to w_pre)."""
     if isinstance(x, (tuple, list)):
         n, d = x[0].shape
-        codes, scales = _want_act8(x, n, d, x[0])
-        like, x = x[0], None
+        dev = x[0].get_device()
+        codes, scales = _arg_act8(x, n, d, dev)
+        px = None
     else:
         n, d = x.shape
-        _want("x", x, (n, d), (x_dt,), x)
-        like = x
+        dev = x.get_device()
+        codes = scales = None
+        px = _arg("x", x, (n, d), x_dt, dev)
     mode = MOM_GATE_NONE
-    _want("y", y, (n, d), (dt,), like)
     if gate is not None:
-        elem = gate.dim() == 2 and tuple(gate.shape) == (n, d) and d > 1
-        mode = MOM_GATE_ELEMENT if elem else MOM_GATE_TOKEN
-        if not elem and tuple(gate.shape) not in ((n,), (n, 1)):
-            raise ValueError("MoM: gate has shape %s, (%d,), (%d, 1) or (%d, %d) is wanted"
-                             % (tuple(gate.shape), n, n, n, d))
-        _want("gate", gate, gate.shape, (dt,), like)
-    for name, w in (("w_post", w_post), ("res_scale", res_scale), ("w_pre", w_pre)):
-        _want(name, w, (d,), _F32, like)
-    return like, x, codes, scales, mode, n, d
+        g = gate.shape
+        mode = MOM_GATE_ELEMENT if g == (n, d) and d > 1 else MOM_GATE_TOKEN
+        if mode == MOM_GATE_TOKEN and g != (n, 1) and g != (n,):
+            raise ValueError("MoM: gate has shape %s, (%d,), (%d, 1) or (%d, %d) is wanted" % (tuple(g), n, n, n, d))
+        gate = _arg("gate", gate, g, dt, dev)
+    w = (d,)
+    return dev, n, d, (px, codes, scales, _arg("y", y, (n, d), dt, dev), gate, mode, _arg("w_post", w_post, w, _F32, dev),
+                       _arg("res_scale", res_scale, w, _F32, dev), _arg("w_pre", w_pre, w, _F32, dev))
 
 
 def mom_residual_norm(x, y, gate, w_post, res_scale, w_pre, eps, x_out, h, pack=None, stream=None):
@@ -716,15 +744,12 @@ def mom_residual_norm(x, y, gate, w_post, res_scale, w_pre, eps, x_out, h, pack=
     res_scale None: 1; x_out, h: None where not wanted; pack: (codes, scales)
     that receive x's 8-bit checkpoint."""
     q8 = isinstance(x, (tuple, list))
-    x_dt = x_out.dtype if q8 and x_out is not None else torch.float32 if q8 else x.dtype
-    dt = next((t.dtype for t in (y, h, gate) if t is not None), x_dt)
-    like, x, codes, scales, mode, n, d = _res_norm(x, y, gate, w_post, res_scale, w_pre, x_dt, dt)
-    _want("x_out", x_out, (n, d), (x_dt,), like)
-    _want("h", h, (n, d), (dt,), like)
-    p_codes, p_scales = _want_act8(pack, n, d, like) if pack is not None else (None, None)
-    _run("mom_residual_norm", like, stream, lib.mom_residual_norm, _p(x), _p(codes), _p(scales), _p(y), _p(gate), mode,
-         _p(w_post), _p(res_scale), _p(w_pre), float(eps), n, d, dtype_code(x_dt), dtype_code(dt), _p(x_out), _p(h),
-         _p(p_codes), _p(p_scales))
+    x_dt = x_out.dtype if q8 and x_out is not None else _F32 if q8 else x.dtype
+    dt = y.dtype if y is not None else h.dtype if h is not None else gate.dtype if gate is not None else x_dt
+    dev, n, d, ops = _arg_norm(x, y, gate, w_post, res_scale, w_pre, x_dt, dt)
+    codes, scales = _arg_act8(pack, n, d, dev) if pack is not None else (None, None)
+    _launch("mom_residual_norm", lib.mom_residual_norm, dev, stream, *ops, eps, n, d, dtype_code(x_dt), dtype_code(dt),
+            _arg("x_out", x_out, (n, d), x_dt, dev), _arg("h", h, (n, d), dt, dev), codes, scales)
 
 
 def mom_residual_norm_bwd_workspace_size(n_rows, d):
@@ -736,56 +761,43 @@ def mom_residual_norm_bwd(x, y, gate, w_post, res_scale, w_pre, eps, dx_out, dh,
     """The adjoint of mom_residual_norm at the same x, y, gate and weights:
     from dx_out and dh (None: 0 / no pre-norm) the gradients dx, dy, dgate (the
     gate's shape), dw_post, dres_scale, dw_pre (None where not wanted)."""
-    q8 = isinstance(x, (tuple, list))
-    x_dt = torch.float32 if q8 else x.dtype
-    dt = next((t.dtype for t in (y, dy, gate) if t is not None), x_dt)
-    like, x, codes, scales, mode, n, d = _res_norm(x, y, gate, w_post, res_scale, w_pre, x_dt, dt)
-    g_dt = dx.dtype
-    for name, t in (("dx_out", dx_out), ("dh", dh), ("dx", dx)):
-        _want(name, t, (n, d), (g_dt,), like)
-    _want("dy", dy, (n, d), (dt,), like)
-    if dgate is not None and gate is not None:
-        _want("dgate", dgate, gate.shape, (dt,), like)
-    for name, t in (("dw_post", dw_post), ("dres_scale", dres_scale), ("dw_pre", dw_pre)):
-        _want(name, t, (d,), _F32, like)
-    _run("mom_residual_norm_bwd", like, stream, lib.mom_residual_norm_bwd, _p(x), _p(codes), _p(scales), _p(y),
-         _p(gate), mode, _p(w_post), _p(res_scale), _p(w_pre), float(eps), n, d, dtype_code(x_dt), dtype_code(dt),
-         _p(dx_out), _p(dh), dtype_code(g_dt), _p(dx), _p(dy), _p(dgate), _p(dw_post), _p(dres_scale), _p(dw_pre),
-         _p(ws), ws.numel())
+    x_dt = _F32 if isinstance(x, (tuple, list)) else x.dtype
+    dt = y.dtype if y is not None else dy.dtype if dy is not None else gate.dtype if gate is not None else x_dt
+    dev, n, d, ops = _arg_norm(x, y, gate, w_post, res_scale, w_pre, x_dt, dt)
+    g_dt, rows, w = dx.dtype, (n, d), (d,)
+    if dgate is not None:
+        dgate = _arg("dgate", dgate, dgate.shape if gate is None else gate.shape, dt, dev)
+    _launch("mom_residual_norm_bwd", lib.mom_residual_norm_bwd, dev, stream, *ops, eps, n, d, dtype_code(x_dt),
+            dtype_code(dt), _arg("dx_out", dx_out, rows, g_dt, dev), _arg("dh", dh, rows, g_dt, dev), dtype_code(g_dt),
+            _arg("dx", dx, rows, g_dt, dev), _arg("dy", dy, rows, dt, dev),
+            dgate, _arg("dw_post", dw_post, w, _F32, dev), _arg("dres_scale", dres_scale, w, _F32, dev),
+            _arg("dw_pre", dw_pre, w, _F32, dev), _arg_ws(ws, dev), ws.numel())
 
 
 def mom_linear_ce_workspace_size(n_rows, d, vocab, dt, backward):
     return lib.mom_linear_ce_workspace_size(n_rows, d, vocab, dtype_code(dt), int(bool(backward)))
 
 
-def _want_ce(x, w, targets):
+def _arg_ce(x, w, targets):
     n, d = x.shape
-    vocab = w.shape[0]
-    _want("x", x, (n, d), _ANY, x)
-    _want("w", w, (vocab, d), (x.dtype,), x)
-    _want("targets", targets, (n,), (torch.int32,), x)
-    return n, d, vocab
+    vocab, dev, dt = w.shape[0], x.get_device(), x.dtype
+    return dev, n, d, vocab, dt, (_arg("x", x, (n, d), dt, dev), _arg("w", w, (vocab, d), dt, dev),
+                                  _arg("targets", targets, (n,), torch.int32, dev))
 
 
 def mom_linear_ce_fwd(x, w, targets, loss, lse, mean, ws, stream=None):
     """loss, lse [n] of the logits x w^T (x [n, d], w [vocab, d], targets [n]
     int32, < 0: padding); mean [2] float32 or None: mean loss, 1 / rows counted."""
-    n, d, vocab = _want_ce(x, w, targets)
-    _want("loss", loss, (n,), _F32, x)
-    _want("lse", lse, (n,), _F32, x)
-    _want("mean", mean, (2,), _F32, x)
-    _run("mom_linear_ce_fwd", x, stream, lib.mom_linear_ce_fwd, _p(x), _p(w), _p(targets), dtype_code(x.dtype), n, d,
-         vocab, _p(loss), _p(lse), _p(mean), _p(ws), ws.numel())
+    dev, n, d, vocab, dt, ops = _arg_ce(x, w, targets)
+    _launch("mom_linear_ce_fwd", lib.mom_linear_ce_fwd, dev, stream, *ops, dtype_code(dt), n, d, vocab,
+            _arg("loss", loss, (n,), _F32, dev), _arg("lse", lse, (n,), _F32, dev), _arg("mean", mean, (2,), _F32, dev),
+            _arg_ws(ws, dev), ws.numel())
 
 
 def mom_linear_ce_bwd(x, w, targets, lse, dloss, dscale, dx, dw, ws, stream=None):
     """dx [n, d] and dw [vocab, d] of sum_t dloss[t] dscale loss[t] (dloss [n],
     dscale [1]; None: 1), lse from the forward."""
-    n, d, vocab = _want_ce(x, w, targets)
-    _want("lse", lse, (n,), _F32, x)
-    _want("dloss", dloss, (n,), _F32, x)
-    _want("dscale", dscale, (1,), _F32, x)
-    _want("dx", dx, (n, d), (x.dtype,), x)
-    _want("dw", dw, (vocab, d), (x.dtype,), x)
-    _run("mom_linear_ce_bwd", x, stream, lib.mom_linear_ce_bwd, _p(x), _p(w), _p(targets), _p(lse), _p(dloss),
-         _p(dscale), dtype_code(x.dtype), n, d, vocab, _p(dx), _p(dw), _p(ws), ws.numel())
+    dev, n, d, vocab, dt, ops = _arg_ce(x, w, targets)
+    _launch("mom_linear_ce_bwd", lib.mom_linear_ce_bwd, dev, stream, *ops, _arg("lse", lse, (n,), _F32, dev),
+            _arg("dloss", dloss, (n,), _F32, dev), _arg("dscale", dscale, (1,), _F32, dev), dtype_code(dt), n, d, vocab,
+            _arg("dx", dx, (n, d), dt, dev), _arg("dw", dw, (vocab, d), dt, dev), _arg_ws(ws, dev), ws.numel())

@@ -25,36 +25,45 @@ class LMHead:
         self.w = weight
         self.vocab, self.d_model = weight.shape
         self.dtype, self.device = weight.dtype, weight.device
-        self._bufs = {}
-        self._held = []
+        self._bufs, self._ws, self._held = {}, {}, []
 
-    def _buf(self, name, shape, dtype):
-        key = (name, tuple(shape), dtype)
-        t = self._bufs.get(key)
-        if t is None:
-            t = self._bufs[key] = torch.empty(shape, dtype=dtype, device=self.device)
-        return t
+    def _fwd_bufs(self, n):
+        b = self._bufs.get(("fwd", n))
+        if b is None:
+            new = lambda k: torch.empty(k, dtype=torch.float32, device=self.device)
+            loss, lse, mean = new(n), new(n), new(2)
+            size = B.mom_linear_ce_workspace_size(n, self.d_model, self.vocab, self.dtype, False)
+            b = self._bufs["fwd", n] = (loss, lse, mean, mean[0], mean[1], mean[1:2], size)
+        return b
 
-    def _ws(self, name, nbytes, stream):
-        key = ("ws", name)
-        t = self._bufs.get(key)
-        with torch.cuda.stream(stream):            # None: the current stream
-            if t is None or t.numel() < nbytes:
-                t = self._bufs[key] = B.new_workspace(nbytes, self.device)
-            if torch.cuda.is_current_stream_capturing() and not any(t is h for h in self._held):
-                self._held.append(t)    # a graph keeps its workspace when a larger one takes its place
+    def _bwd_bufs(self, n):
+        b = self._bufs.get(("bwd", n))
+        if b is None:
+            new = lambda k: torch.empty((k, self.d_model), dtype=self.dtype, device=self.device)
+            if "dw" not in self._bufs:
+                self._bufs["dw"] = new(self.vocab)
+            size = B.mom_linear_ce_workspace_size(n, self.d_model, self.vocab, self.dtype, True)
+            b = self._bufs["bwd", n] = (new(n), self._bufs["dw"], size)
+        return b
+
+    def _workspace(self, name, nbytes, stream):
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self._workspace(name, nbytes, None)
+        t = self._ws.get(name)
+        if t is None or t.numel() < nbytes:
+            t = self._ws[name] = B.new_workspace(nbytes, self.device)
+        if torch.cuda.is_current_stream_capturing() and not any(t is h for h in self._held):
+            self._held.append(t)    # a graph keeps its workspace when a larger one takes its place
         return t
 
     def loss(self, x: torch.Tensor, targets: torch.Tensor, stream=None) -> Dict[str, torch.Tensor]:
         """x [N, d_model], targets [N] int32 (negative: padding).  Returns
         ``loss`` [N] (0 for padding), ``lse`` [N], the ``mean`` loss over the
         rows with a target and ``inv_count`` = 1 / their number (0-d)."""
-        n = x.shape[0]
-        loss, lse = self._buf("loss", (n,), torch.float32), self._buf("lse", (n,), torch.float32)
-        mean = self._buf(("mean", n), (2,), torch.float32)
-        ws = self._ws("fwd", B.mom_linear_ce_workspace_size(n, self.d_model, self.vocab, self.dtype, False), stream)
-        B.mom_linear_ce_fwd(x, self.w, targets, loss, lse, mean, ws, stream=stream)
-        return dict(loss=loss, lse=lse, mean=mean[0], inv_count=mean[1])
+        loss, lse, both, mean, inv_count, _, size = self._fwd_bufs(x.shape[0])
+        B.mom_linear_ce_fwd(x, self.w, targets, loss, lse, both, self._workspace("fwd", size, stream), stream=stream)
+        return dict(loss=loss, lse=lse, mean=mean, inv_count=inv_count)
 
     def backward(self, x: torch.Tensor, targets: torch.Tensor, dloss: Optional[torch.Tensor] = None,
                  stream=None) -> Dict[str, torch.Tensor]:
@@ -63,22 +72,19 @@ class LMHead:
         weight's type, of the mean loss, or with dloss [N] float32 of
         sum(dloss * loss)."""
         n = x.shape[0]
-        lse = self._bufs.get(("lse", (n,), torch.float32))
-        if lse is None:
+        fwd = self._bufs.get(("fwd", n))
+        if fwd is None:
             raise ValueError("backward follows a loss call of the same shape")
-        scale = None if dloss is not None else self._buf(("mean", n), (2,), torch.float32)[1:2]
-        dx = self._buf("dx", (n, self.d_model), self.dtype)
-        dw = self._buf("dw", (self.vocab, self.d_model), self.dtype)
-        ws = self._ws("bwd", B.mom_linear_ce_workspace_size(n, self.d_model, self.vocab, self.dtype, True), stream)
-        B.mom_linear_ce_bwd(x, self.w, targets, lse, dloss, scale, dx, dw, ws, stream=stream)
+        dx, dw, size = self._bwd_bufs(n)
+        B.mom_linear_ce_bwd(x, self.w, targets, fwd[1], dloss, None if dloss is not None else fwd[5], dx, dw,
+                            self._workspace("bwd", size, stream), stream=stream)
         return dict(dx=dx, dw=dw)
 
     def device_errors(self):
         """(code, info) of every workspace with a recorded violation."""
         errs = {}
-        for key, t in self._bufs.items():
-            if key[0] == "ws":
-                code, info = B.mom_get_error(t)
-                if code:
-                    errs[key[1]] = (code, info)
+        for name, t in self._ws.items():
+            code, info = B.mom_get_error(t)
+            if code:
+                errs[name] = (code, info)
         return errs

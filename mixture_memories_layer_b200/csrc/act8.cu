@@ -28,21 +28,62 @@ __device__ __forceinline__ Where where(int64_t u, int chunks) {
     return w;
 }
 
-template <typename T, bool VEC, bool FLAT>
-__global__ void __launch_bounds__(kThreads) act8_pack_kernel(const T* __restrict__ x, int64_t total, int d, int chunks,
-                                                             int groups, int8_t* __restrict__ codes,
-                                                             float* __restrict__ scales) {
+// Rows that 16-byte copies can take: kAhead chunks of a warp are in flight to
+// slots in shared memory, of which each thread reads what it copied itself.
+constexpr int kAhead = 5, kSlots = kAhead + 1;
+template <typename T, bool FLAT>
+__global__ void __launch_bounds__(kThreads, 4) act8_pack_kernel(const T* __restrict__ x, int64_t total, int d, int chunks,
+                                                                int groups, int8_t* __restrict__ codes,
+                                                                float* __restrict__ scales) {
+    typedef Raw8<T, true> R;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int lane = threadIdx.x & 31;
+    const uint32_t pitch = kThreads * 16, base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+    const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
+    int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int dd = FLAT ? kChunk : d;
+    auto put = [&](int64_t v, int slot) {
+        if (v < total) {
+            const Where w = FLAT ? Where{v, 0} : where(v, chunks);
+            R::copy(base + slot * R::PIECES * pitch, pitch, x + w.row * dd, w.c0, dd, lane);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) put(u + k * step, k);
+    int in = kAhead, out = 0;
+    for (; u < total; u += step) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        R r;
+        r.take(base + out * R::PIECES * pitch, pitch);
+        put(u + kAhead * step, in);
+        in = in + 1 == kSlots ? 0 : in + 1;
+        out = out + 1 == kSlots ? 0 : out + 1;
+        const Where w = FLAT ? Where{u, 0} : where(u, chunks);
+        float f[8];
+        uint32_t m[2];
+        r.get(f);
+        r.amax(m);
+        act8_store<true>(f, m, w.c0, dd, lane, codes + w.row * dd, scales + w.row * (FLAT ? 2 : groups));
+    }
+}
+
+// Other rows: kUnroll chunks of a warp loaded at a time.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) act8_pack_odd_kernel(const T* __restrict__ x, int64_t total, int d, int chunks,
+                                                                 int groups, int8_t* __restrict__ codes,
+                                                                 float* __restrict__ scales) {
     const int lane = threadIdx.x & 31;
     const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
     for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < total; u += step * kUnroll) {
-        Raw8<T, VEC> r[kUnroll];
+        Raw8<T, false> r[kUnroll];
         Where w[kUnroll];
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) {
             const int64_t v = u + k * step;
             if (v < total) {
-                w[k] = FLAT ? Where{v, 0} : where(v, chunks);
-                r[k].load(x + w[k].row * (FLAT ? kChunk : d), w[k].c0, FLAT ? kChunk : d, lane);
+                w[k] = where(v, chunks);
+                r[k].load(x + w[k].row * d, w[k].c0, d, lane);
             }
         }
 #pragma unroll
@@ -52,8 +93,7 @@ __global__ void __launch_bounds__(kThreads) act8_pack_kernel(const T* __restrict
                 uint32_t m[2];
                 r[k].get(f);
                 r[k].amax(m);
-                act8_store<VEC>(f, m, w[k].c0, FLAT ? kChunk : d, lane, codes + w[k].row * (FLAT ? kChunk : d),
-                                scales + w[k].row * (FLAT ? 2 : groups));
+                act8_store<false>(f, m, w[k].c0, d, lane, codes + w[k].row * d, scales + w[k].row * groups);
             }
         }
     }
@@ -88,12 +128,25 @@ __global__ void __launch_bounds__(kThreads) act8_unpack_kernel(const int8_t* __r
     }
 }
 
-unsigned grid_for(int64_t units) {
+// `ctas` an SM at most
+unsigned grid_for(int64_t units, int ctas) {
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t want = cdiv(units, kThreads / 32), most = (int64_t)sms * 8;
+    const int64_t want = cdiv(units, kThreads / 32), most = (int64_t)sms * ctas;
     return (unsigned)(want < most ? want : most);
+}
+
+template <typename T, bool FLAT>
+cudaError_t run_pack(const void* x, int64_t total, int d, int chunks, int groups, int8_t* codes, float* scales,
+                     cudaStream_t st) {
+    constexpr int SMEM = kSlots * Raw8<T, true>::PIECES * kThreads * 16;
+    auto* kernel = act8_pack_kernel<T, FLAT>;
+    static unsigned long long optin_done = 0;
+    const cudaError_t e = smem_optin((const void*)kernel, SMEM, &optin_done);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid_for(total, 4), kThreads, SMEM, st>>>(reinterpret_cast<const T*>(x), total, d, chunks, groups, codes, scales);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -102,16 +155,17 @@ cudaError_t launch_act8_pack(const void* x, int dt, int64_t n_rows, int d, int8_
                              cudaStream_t st) {
     const int chunks = (int)cdiv(d, kChunk), groups = (int)cdiv(d, kActGroup);
     const int64_t total = n_rows * chunks;
-    const unsigned grid = grid_for(total);
     const bool flat = vec && d % kChunk == 0;
-#define MOM_PACK(T, V, F) \
-    act8_pack_kernel<T, V, F><<<grid, kThreads, 0, st>>>(reinterpret_cast<const T*>(x), total, d, chunks, groups, codes, scales)
-#define MOM_PACK_T(T) do { if (flat) MOM_PACK(T, true, true); else if (vec) MOM_PACK(T, true, false); else MOM_PACK(T, false, false); } while (0)
-    if (dt == MOM_BF16) MOM_PACK_T(bf16);
-    else MOM_PACK_T(float);
-#undef MOM_PACK_T
-#undef MOM_PACK
     count_launches(1);
+    if (dt == MOM_BF16) {
+        if (flat) return run_pack<bf16, true>(x, total, d, chunks, groups, codes, scales, st);
+        if (vec) return run_pack<bf16, false>(x, total, d, chunks, groups, codes, scales, st);
+        act8_pack_odd_kernel<bf16><<<grid_for(total, 8), kThreads, 0, st>>>(reinterpret_cast<const bf16*>(x), total, d, chunks, groups, codes, scales);
+    } else {
+        if (flat) return run_pack<float, true>(x, total, d, chunks, groups, codes, scales, st);
+        if (vec) return run_pack<float, false>(x, total, d, chunks, groups, codes, scales, st);
+        act8_pack_odd_kernel<float><<<grid_for(total, 8), kThreads, 0, st>>>(reinterpret_cast<const float*>(x), total, d, chunks, groups, codes, scales);
+    }
     return cudaGetLastError();
 }
 
@@ -119,7 +173,7 @@ cudaError_t launch_act8_unpack(const int8_t* codes, const float* scales, int64_t
                                bool vec, cudaStream_t st) {
     const int chunks = (int)cdiv(d, kChunk), groups = (int)cdiv(d, kActGroup);
     const int64_t total = n_rows * chunks;
-    const unsigned grid = grid_for(total);
+    const unsigned grid = grid_for(total, 8);
     const bool flat = vec && d % kChunk == 0;
 #define MOM_UNPACK(T, V, F) \
     act8_unpack_kernel<T, V, F><<<grid, kThreads, 0, st>>>(codes, scales, total, d, chunks, groups, reinterpret_cast<T*>(x))

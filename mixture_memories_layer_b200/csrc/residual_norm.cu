@@ -53,24 +53,36 @@ __device__ __forceinline__ float sigmoid(float z, float& rest) {
     rest = z > 0.f ? e * s : 1.f - s;
     return s;
 }
-__device__ __forceinline__ float sigmoid(float z) { return fast_rcp(1.f + fast_ex2(z * -1.4426950408889634f)); }
+__device__ __forceinline__ void sigmoid(f2 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        split(mul2(v[i], both(-1.4426950408889634f)), a, b);
+        split(add2(make_f2(fast_ex2(a), fast_ex2(b)), both(1.f)), a, b);
+        v[i] = make_f2(fast_rcp(a), fast_rcp(b));
+    }
+}
 
 constexpr int kMaxWarps = 16;      // of a row
 
 // Sums of K values over the W warps of a row (every thread gets them), in warp
-// order; one warp a row needs no barrier.
+// order; one warp a row needs no barrier.  buf [K][kMaxWarps] holds zeros past
+// warp W.
 template <int K> __device__ __forceinline__ void row_sum(float (&v)[K], float* buf, int W, int warp, int lane) {
     warp_sum_n<K>(v);
     if (W == 1) return;
     if (lane == 0)
 #pragma unroll
-        for (int k = 0; k < K; ++k) buf[warp * K + k] = v[k];
+        for (int k = 0; k < K; ++k) buf[k * kMaxWarps + warp] = v[k];
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = 0.f;
-    for (int i = 0; i < W; ++i)
+    for (int i = 0; i < W; i += 4)
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += buf[i * K + k];
+        for (int k = 0; k < K; ++k) {
+            const float4 p = *reinterpret_cast<const float4*>(buf + k * kMaxWarps + i);
+            v[k] += (p.x + p.y) + (p.z + p.w);
+        }
 }
 
 // The column weights of a thread's channels, res_scale * w_post and w_pre: in
@@ -78,38 +90,43 @@ template <int K> __device__ __forceinline__ void row_sum(float (&v)[K], float* b
 // (from L1) at each use.
 template <bool VEC, int C> struct Weights {
     static constexpr bool KEEP = C == 1;
-    float post[KEEP ? 8 : 1], pre[KEEP ? 8 : 1];
-    static __device__ __forceinline__ void read_post(const ResNormArgs& a, int c0, int lane, float* w) {
-        load8<VEC>(a.w_post, c0, a.d, lane, w);
+    f2 post[KEEP ? 4 : 1], pre[KEEP ? 4 : 1];
+    static __device__ __forceinline__ void read(const float* from, const ResNormArgs& a, int c0, int lane, f2 (&w)[4]) {
+        float v[8];
+        load8<VEC>(from, c0, a.d, lane, v);
+        get_f2(v, w);
+    }
+    static __device__ __forceinline__ void read_post(const ResNormArgs& a, int c0, int lane, f2 (&w)[4]) {
+        read(a.w_post, a, c0, lane, w);
         if (a.res_scale) {
-            float s[8];
-            load8<VEC>(a.res_scale, c0, a.d, lane, s);
+            f2 s[4];
+            read(a.res_scale, a, c0, lane, s);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] *= s[i];
+            for (int i = 0; i < 4; ++i) w[i] = mul2(w[i], s[i]);
         }
     }
     __device__ __forceinline__ Weights(const ResNormArgs& a, bool has_pre, int c0, int lane) {
         if constexpr (KEEP) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) post[i] = pre[i] = 0.f;
+            for (int i = 0; i < 4; ++i) post[i] = pre[i] = 0ull;
             if (a.y) read_post(a, c0, lane, post);
-            if (has_pre) load8<VEC>(a.w_pre, c0, a.d, lane, pre);
+            if (has_pre) read(a.w_pre, a, c0, lane, pre);
         }
     }
-    __device__ __forceinline__ void get_post(const ResNormArgs& a, int c0, int lane, float* w) const {
+    __device__ __forceinline__ void get_post(const ResNormArgs& a, int c0, int lane, f2 (&w)[4]) const {
         if constexpr (KEEP) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = post[i];
+            for (int i = 0; i < 4; ++i) w[i] = post[i];
         } else {
             read_post(a, c0, lane, w);
         }
     }
-    __device__ __forceinline__ void get_pre(const ResNormArgs& a, int c0, int lane, float* w) const {
+    __device__ __forceinline__ void get_pre(const ResNormArgs& a, int c0, int lane, f2 (&w)[4]) const {
         if constexpr (KEEP) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = pre[i];
+            for (int i = 0; i < 4; ++i) w[i] = pre[i];
         } else {
-            load8<VEC>(a.w_pre, c0, a.d, lane, w);
+            read(a.w_pre, a, c0, lane, w);
         }
     }
 };
@@ -124,6 +141,18 @@ template <bool VEC, int C> struct Weights {
 //   DIRECT  loads when the row's turn comes, its lines asked into L2 one row
 //           ahead.  Wider rows are read at each use, the later ones from L1.
 enum Source { RING, REGS, DIRECT };
+
+template <typename R> __device__ __forceinline__ void take_f2(const R& r, f2 (&v)[4]) {
+    float f[8];
+    r.get(f);
+    get_f2(f, v);
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_f2(T* row, int c0, int d, int lane, const f2 (&v)[4]) {
+    float f[8];
+    put_f2(v, f);
+    store8<VEC>(row, c0, d, lane, f);
+}
 
 __device__ __forceinline__ void ask_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
@@ -233,29 +262,29 @@ template <typename XT, typename T, typename G, bool VEC, int C, bool HAS_Y, bool
         if constexpr (C == 1) o = cur.x;
         else o.load(a, row, c0(j), lane);
     }
-    __device__ __forceinline__ void y(int j, float* v) const {
-        if constexpr (C == 1) { cur.y.get(v); return; }
+    __device__ __forceinline__ void y(int j, f2 (&v)[4]) const {
+        if constexpr (C == 1) { take_f2(cur.y, v); return; }
         Y o;
         o.load(at_y(row), c0(j), a.d, lane);
-        o.get(v);
+        take_f2(o, v);
     }
-    __device__ __forceinline__ void g(int j, float* v) const {
-        if constexpr (C == 1) { cur.g.get(v); return; }
+    __device__ __forceinline__ void g(int j, f2 (&v)[4]) const {
+        if constexpr (C == 1) { take_f2(cur.g, v); return; }
         Y o;
         o.load(at_g(row), c0(j), a.d, lane);
-        o.get(v);
+        take_f2(o, v);
     }
-    __device__ __forceinline__ void h(int j, float* v) const {
-        if constexpr (C == 1) { cur.h.get(v); return; }
+    __device__ __forceinline__ void h(int j, f2 (&v)[4]) const {
+        if constexpr (C == 1) { take_f2(cur.h, v); return; }
         D o;
         o.load(at_h(row), c0(j), a.d, lane);
-        o.get(v);
+        take_f2(o, v);
     }
-    __device__ __forceinline__ void d(int j, float* v) const {
-        if constexpr (C == 1) { cur.d.get(v); return; }
+    __device__ __forceinline__ void d(int j, f2 (&v)[4]) const {
+        if constexpr (C == 1) { take_f2(cur.d, v); return; }
         D o;
         o.load(at_d(row), c0(j), a.d, lane);
-        o.get(v);
+        take_f2(o, v);
     }
 };
 
@@ -265,7 +294,8 @@ template <typename XT, typename T, bool VEC, int C, bool HAS_Y, int SRC, int MAX
 __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : SRC != RING ? 2 : HAS_Y ? 3 : 4)
 residual_norm_kernel(const ResNormArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float red[2][2][kMaxWarps];
+    __shared__ __align__(16) float red[2][2][kMaxWarps];
+    if (threadIdx.x < 4 * kMaxWarps) (&red[0][0][0])[threadIdx.x] = 0.f;
     const int lane = threadIdx.x & 31, W = a.warps_per_row, warp = W > 1 ? threadIdx.x >> 5 : 0;
     const int rows_cta = W > 1 ? 1 : blockDim.x >> 5;
     const int64_t step = (int64_t)gridDim.x * rows_cta;
@@ -277,71 +307,82 @@ residual_norm_kernel(const ResNormArgs a) {
     T gate_next = from_f<T>(0.f);
     if (a.gate_mode == MOM_GATE_TOKEN && first < a.n_rows) gate_next = reinterpret_cast<const T*>(a.gate)[first];
     const Weights<VEC, C> wt(a, a.h != nullptr, warp * kChunk, lane);
+    __syncthreads();
     for (int buf = 0; in.row < a.n_rows; in.row += in.step, buf ^= 1) {      // the same count in all warps of a row
-        const int64_t row = in.row;
+        const int64_t row = in.row, at = row * d;
         in.begin();
         const T gate = gate_next;
         if (a.gate_mode == MOM_GATE_TOKEN && row + step < a.n_rows)
             gate_next = reinterpret_cast<const T*>(a.gate)[row + step];
-        float xv[C][8], ry = 0.f, ss[1] = {0.f};
+        f2 xv[C][4];
+        float ry = 0.f, ss[1];
         if (HAS_Y) {
+            f2 q = 0ull;
 #pragma unroll
             for (int j = 0; j < C; ++j) {
-                float y[8];
+                f2 y[4];
                 in.y(j, y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss[0] = fmaf(y[i], y[i], ss[0]);
+                for (int i = 0; i < 4; ++i) q = fma2(y[i], y[i], q);
             }
+            ss[0] = sum2(q);
             row_sum<1>(ss, red[buf][0], W, warp, lane);
             ry = rsqrtf(ss[0] * inv_d + a.eps);                     // 1 / rms(y), times a token's gate
-            if (a.gate_mode == MOM_GATE_TOKEN) ry *= sigmoid(to_f(gate));
+            if (a.gate_mode == MOM_GATE_TOKEN) {
+                float rest;
+                ry *= sigmoid(to_f(gate), rest);
+            }
         }
-        ss[0] = 0.f;
+        f2 q = 0ull;
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             const int c0 = in.c0(j);
             RawX<XT, VEC> x;
             in.x(j, x);
-            x.get(xv[j]);
+            take_f2(x, xv[j]);
             if constexpr (!std::is_same<XT, Q8>::value) {
                 if (a.codes_out) {
                     uint32_t m[2];
+                    float f[8];
                     x.amax(m);
-                    act8_store<VEC>(xv[j], m, c0, d, lane, a.codes_out + row * d, a.scales_out + row * a.groups);
+                    put_f2(xv[j], f);
+                    act8_store<VEC>(f, m, c0, d, lane, a.codes_out + at, a.scales_out + row * a.groups);
                 }
             }
             if (HAS_Y) {
-                float y[8], w[8];
+                f2 y[4], w[4];
                 in.y(j, y);
                 wt.get_post(a, c0, lane, w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] *= ry;
+                for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], both(ry));
                 if (a.gate_mode == MOM_GATE_ELEMENT) {
-                    float g[8];
+                    f2 g[4];
                     in.g(j, g);
+                    sigmoid(g);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] *= sigmoid(g[i]);
+                    for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], g[i]);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) xv[j][i] = fmaf(y[i], w[i], xv[j][i]);
+                for (int i = 0; i < 4; ++i) xv[j][i] = fma2(y[i], w[i], xv[j][i]);
             }
             if (a.x_out) {
-                if (a.x_out_f32) store8<VEC>(reinterpret_cast<float*>(a.x_out) + row * d, c0, d, lane, xv[j]);
-                else store8<VEC>(reinterpret_cast<bf16*>(a.x_out) + row * d, c0, d, lane, xv[j]);
+                if (a.x_out_f32) store_f2<VEC>(reinterpret_cast<float*>(a.x_out) + at, c0, d, lane, xv[j]);
+                else store_f2<VEC>(reinterpret_cast<bf16*>(a.x_out) + at, c0, d, lane, xv[j]);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss[0] = fmaf(xv[j][i], xv[j][i], ss[0]);
+            for (int i = 0; i < 4; ++i) q = fma2(xv[j][i], xv[j][i], q);
         }
         if (a.h) {
+            ss[0] = sum2(q);
             row_sum<1>(ss, red[buf][1], W, warp, lane);
-            const float rx = rsqrtf(ss[0] * inv_d + a.eps);
+            const f2 rx = both(rsqrtf(ss[0] * inv_d + a.eps));
 #pragma unroll
             for (int j = 0; j < C; ++j) {
-                float w[8];
+                f2 w[4];
                 wt.get_pre(a, in.c0(j), lane, w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) xv[j][i] *= rx * w[i];
-                store8<VEC>(reinterpret_cast<T*>(a.h) + row * d, in.c0(j), d, lane, xv[j]);
+                for (int i = 0; i < 4; ++i) xv[j][i] = mul2(mul2(xv[j][i], rx), w[i]);
+                store_f2<VEC>(reinterpret_cast<T*>(a.h) + at, in.c0(j), d, lane, xv[j]);
             }
         }
     }
@@ -355,105 +396,108 @@ residual_norm_kernel(const ResNormArgs a) {
 template <typename XT, typename T, typename G, bool VEC, int C, int SRC, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : 2)
 residual_norm_bwd_kernel(const ResNormArgs a, const ResNormBwdArgs b) {
-    __shared__ float red[2][4][kMaxWarps];
+    __shared__ __align__(16) float red[2][4][kMaxWarps];
+    for (int i = threadIdx.x; i < 8 * kMaxWarps; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     const int d = a.d;
     const float inv_d = 1.f / (float)d;
-    float accA[C][8], accP[C][8];
+    f2 accA[C][4], accP[C][4];
 #pragma unroll
     for (int j = 0; j < C; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) accA[j][i] = accP[j][i] = 0.f;
+        for (int i = 0; i < 4; ++i) accA[j][i] = accP[j][i] = 0ull;
     Rows<XT, T, G, VEC, C, true, true, SRC> in(a, b, nullptr, W, warp, lane, blockIdx.x, gridDim.x);
     T gate_next = from_f<T>(0.f);
     if (a.gate_mode == MOM_GATE_TOKEN && in.row < a.n_rows) gate_next = reinterpret_cast<const T*>(a.gate)[in.row];
     const Weights<VEC, C> wt(a, b.dh != nullptr, warp * kChunk, lane);
+    __syncthreads();
     for (int buf = 0; in.row < a.n_rows; in.row += in.step, buf ^= 1) {
-        const int64_t row = in.row;
+        const int64_t row = in.row, at = row * d;
         in.begin();
         const T gate = gate_next;
         if (a.gate_mode == MOM_GATE_TOKEN && row + in.step < a.n_rows)
             gate_next = reinterpret_cast<const T*>(a.gate)[row + in.step];
-        float yk[C == 1 ? 8 : 1], gk[C == 1 ? 8 : 1], dv[C][8];
+        f2 yk[C == 1 ? 4 : 1], gk[C == 1 ? 4 : 1], dv[C][4];
         float gt = 1.f, rest = 0.f, ry = 0.f;
         if (a.gate_mode == MOM_GATE_TOKEN) gt = sigmoid(to_f(gate), rest);
         // n_y and sigma of chunk j
-        auto form = [&](int j, float* y, float* g) {
+        auto form = [&](int j, f2 (&y)[4], f2 (&g)[4]) {
             in.y(j, y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] *= ry;
+            for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], both(ry));
             if (a.gate_mode == MOM_GATE_ELEMENT) {
                 in.g(j, g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] = sigmoid(g[i]);
+                sigmoid(g);
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] = gt;
+                for (int i = 0; i < 4; ++i) g[i] = both(gt);
             }
         };
-        auto again = [&](int j, float* y, float* g) {
+        auto again = [&](int j, f2 (&y)[4], f2 (&g)[4]) {
             if constexpr (C == 1) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) { y[i] = yk[i]; g[i] = gk[i]; }
+                for (int i = 0; i < 4; ++i) { y[i] = yk[i]; g[i] = gk[i]; }
             } else {
                 form(j, y, g);
             }
         };
         if (a.y) {
-            float ss[1] = {0.f};
+            f2 q = 0ull;
 #pragma unroll
             for (int j = 0; j < C; ++j) {
-                float y[8];
+                f2 y[4];
                 in.y(j, y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss[0] = fmaf(y[i], y[i], ss[0]);
+                for (int i = 0; i < 4; ++i) q = fma2(y[i], y[i], q);
             }
+            float ss[1] = {sum2(q)};
             row_sum<1>(ss, red[buf][0], W, warp, lane);
             ry = rsqrtf(ss[0] * inv_d + a.eps);
             if constexpr (C == 1) form(0, yk, gk);
         }
         if (b.dh) {
-            float ss[2] = {0.f, 0.f};
+            f2 qx = 0ull, qh = 0ull;
 #pragma unroll
             for (int j = 0; j < C; ++j) {                                     // dv: x' for now
-                float h[8], w[8];
+                f2 h[4], w[4];
                 RawX<XT, VEC> x;
                 in.x(j, x);
-                x.get(dv[j]);
+                take_f2(x, dv[j]);
                 if (a.y) {
-                    float y[8], g[8];
+                    f2 y[4], g[4];
                     again(j, y, g);
                     wt.get_post(a, in.c0(j), lane, w);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dv[j][i] = fmaf(y[i] * g[i], w[i], dv[j][i]);
+                    for (int i = 0; i < 4; ++i) dv[j][i] = fma2(mul2(y[i], g[i]), w[i], dv[j][i]);
                 }
                 in.h(j, h);
                 wt.get_pre(a, in.c0(j), lane, w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ss[0] = fmaf(dv[j][i], dv[j][i], ss[0]);
-                    ss[1] = fmaf(dv[j][i], h[i] * w[i], ss[1]);
+                for (int i = 0; i < 4; ++i) {
+                    qx = fma2(dv[j][i], dv[j][i], qx);
+                    qh = fma2(dv[j][i], mul2(h[i], w[i]), qh);
                 }
             }
+            float ss[2] = {sum2(qx), sum2(qh)};
             row_sum<2>(ss, red[buf][1], W, warp, lane);
-            const float rx = rsqrtf(ss[0] * inv_d + a.eps);
-            const float k = ss[1] * inv_d * rx * rx * rx;                     // mean(dn n_x) / rms / rms
+            const float r = rsqrtf(ss[0] * inv_d + a.eps);
+            const f2 rx = both(r), mk = both(-ss[1] * inv_d * r * r * r);     // - mean(dn n_x) / rms / rms
 #pragma unroll
             for (int j = 0; j < C; ++j) {
-                float h[8], w[8], o[8];
+                f2 h[4], w[4], o[4];
                 in.h(j, h);
                 wt.get_pre(a, in.c0(j), lane, w);
                 if (b.dx_out) {
                     in.d(j, o);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = 0.f;
+                    for (int i = 0; i < 4; ++i) o[i] = 0ull;
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float hr = h[i] * rx;
-                    accP[j][i] = fmaf(hr, dv[j][i], accP[j][i]);
-                    dv[j][i] = fmaf(hr, w[i], fmaf(dv[j][i], -k, o[i]));      // D
+                for (int i = 0; i < 4; ++i) {
+                    const f2 hr = mul2(h[i], rx);
+                    accP[j][i] = fma2(hr, dv[j][i], accP[j][i]);
+                    dv[j][i] = fma2(hr, w[i], fma2(dv[j][i], mk, o[i]));      // D
                 }
             }
         } else {
@@ -461,59 +505,62 @@ residual_norm_bwd_kernel(const ResNormArgs a, const ResNormBwdArgs b) {
             for (int j = 0; j < C; ++j) in.d(j, dv[j]);
         }
 #pragma unroll
-        for (int j = 0; j < C; ++j) store8<VEC>(reinterpret_cast<G*>(b.dx) + row * d, in.c0(j), d, lane, dv[j]);
+        for (int j = 0; j < C; ++j) store_f2<VEC>(reinterpret_cast<G*>(b.dx) + at, in.c0(j), d, lane, dv[j]);
         if (a.y) {
-            float ss[1] = {0.f};
+            f2 q = 0ull;
 #pragma unroll
             for (int j = 0; j < C; ++j) {
-                float y[8], g[8], w[8];
+                f2 y[4], g[4], w[4];
                 again(j, y, g);
                 wt.get_post(a, in.c0(j), lane, w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float t = dv[j][i] * g[i];
-                    accA[j][i] = fmaf(t, y[i], accA[j][i]);
-                    dv[j][i] = t * w[i];                                      // u = D s sigma w_post
-                    ss[0] = fmaf(dv[j][i], y[i], ss[0]);
+                for (int i = 0; i < 4; ++i) {
+                    const f2 t = mul2(dv[j][i], g[i]);
+                    accA[j][i] = fma2(t, y[i], accA[j][i]);
+                    dv[j][i] = mul2(t, w[i]);                                 // u = D s sigma w_post
+                    q = fma2(dv[j][i], y[i], q);
                 }
             }
+            float ss[1] = {sum2(q)};
             row_sum<1>(ss, red[buf][3], W, warp, lane);
-            const float m = ss[0] * inv_d * ry;
+            const f2 m = both(-ss[0] * inv_d * ry);
             if (a.gate_mode == MOM_GATE_TOKEN && b.dgate && threadIdx.x == 0)
                 reinterpret_cast<T*>(b.dgate)[row] = from_f<T>(ss[0] * rest);
 #pragma unroll
             for (int j = 0; j < C; ++j) {
-                float y[8], o[8];
+                f2 y[4];
                 if constexpr (C == 1) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = yk[i];
+                    for (int i = 0; i < 4; ++i) y[i] = yk[i];
                 } else {
                     in.y(j, y);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] *= ry;
+                    for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], both(ry));
                 }
                 if (a.gate_mode == MOM_GATE_ELEMENT && b.dgate) {
-                    in.g(j, o);
+                    f2 z[4], o[4];
+                    in.g(j, z);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float q;
-                        sigmoid(o[i], q);
-                        o[i] = dv[j][i] * y[i] * q;
+                    for (int i = 0; i < 4; ++i) {
+                        float z0, z1, r0, r1;
+                        split(z[i], z0, z1);
+                        sigmoid(z0, r0);
+                        sigmoid(z1, r1);
+                        o[i] = mul2(mul2(dv[j][i], y[i]), make_f2(r0, r1));
                     }
-                    // dy may be y and dgate the gate: this thread's own elements, read before
-                    store8<VEC>(reinterpret_cast<T*>(b.dgate) + row * d, in.c0(j), d, lane, o);
+                    store_f2<VEC>(reinterpret_cast<T*>(b.dgate) + at, in.c0(j), d, lane, o);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = fmaf(dv[j][i], ry, -y[i] * m);
-                store8<VEC>(reinterpret_cast<T*>(b.dy) + row * d, in.c0(j), d, lane, o);
+                for (int i = 0; i < 4; ++i) dv[j][i] = fma2(dv[j][i], both(ry), mul2(y[i], m));
+                store_f2<VEC>(reinterpret_cast<T*>(b.dy) + at, in.c0(j), d, lane, dv[j]);
             }
         }
     }
     float* pa = b.partial + (int64_t)blockIdx.x * 2 * d;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-        store8<VEC>(pa, in.c0(j), d, lane, accA[j]);
-        store8<VEC>(pa + d, in.c0(j), d, lane, accP[j]);
+        store_f2<VEC>(pa, in.c0(j), d, lane, accA[j]);
+        store_f2<VEC>(pa + d, in.c0(j), d, lane, accP[j]);
     }
 }
 

@@ -11,6 +11,45 @@
 
 namespace mom {
 
+// Two float32 in a register pair: one instruction for both, rounded as two.
+// These row kernels are bound by issuing instructions as much as by memory.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 make_f2(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f2 both(float a) { return make_f2(a, a); }
+__device__ __forceinline__ void split(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ float sum2(f2 v) {
+    float a, b;
+    split(v, a, b);
+    return a + b;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ void get_f2(const float* v, f2 (&o)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = make_f2(v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ void put_f2(const f2 (&v)[4], float* o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split(v[i], o[2 * i], o[2 * i + 1]);
+}
+
 // 16-byte pieces that a thread keeps for itself in shared memory while their
 // copies are in flight: piece p of a slot at slot + p * pitch, pitch = threads * 16.
 __device__ __forceinline__ void piece_copy16(uint32_t dst, const void* src, bool in) {      // else zeros
@@ -236,22 +275,27 @@ __device__ __forceinline__ void act8_store(const float* v, uint32_t (&m)[2], int
 struct Q8 {};                  // the stream's type tag where it is a checkpoint
 template <bool VEC> struct Raw8Q;
 template <> struct Raw8Q<true> {
-    static constexpr int PIECES = 1;       // 8 bytes of codes, the scale behind them
+    // a piece: all threads' codes, 8 bytes each, then a scale for 16 threads,
+    // which lanes 0 and 16 copy for their half warps
+    static constexpr int PIECES = 1;
     uint2 u;
     float s;
-    static __device__ __forceinline__ void copy(uint32_t slot, uint32_t, const int8_t* codes_row, const float* scales_row,
-                                                int c0, int d, int lane) {
+    static __device__ __forceinline__ void copy(uint32_t slot, uint32_t pitch, const int8_t* codes_row,
+                                                const float* scales_row, int c0, int d, int lane) {
         const int c = c0 + lane * 8;
+        const uint32_t at = slot - threadIdx.x * 8;
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;"
-                     ::"r"(slot), "l"(codes_row + (c < d ? c : 0)), "r"(c < d ? 8 : 0) : "memory");
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
-                     ::"r"(slot + 8), "l"(scales_row + (c < d ? c0 / kActGroup + (lane >> 4) : 0)), "r"(c < d ? 4 : 0)
-                     : "memory");
+                     ::"r"(at), "l"(codes_row + (c < d ? c : 0)), "r"(c < d ? 8 : 0) : "memory");
+        if ((lane & 15) == 0)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                         ::"r"(slot - threadIdx.x * 16 + pitch / 2 + (threadIdx.x >> 4) * 4),
+                           "l"(scales_row + (c < d ? c / kActGroup : 0)), "r"(c < d ? 4 : 0) : "memory");
     }
-    __device__ __forceinline__ void take(uint32_t slot, uint32_t) {
-        const uint4 p = piece_read(slot);
-        u = make_uint2(p.x, p.y);
-        s = __uint_as_float(p.z);
+    __device__ __forceinline__ void take(uint32_t slot, uint32_t pitch) {
+        __syncwarp();
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(u.x), "=r"(u.y) : "r"(slot - threadIdx.x * 8) : "memory");
+        asm volatile("ld.shared.f32 %0, [%1];"
+                     : "=f"(s) : "r"(slot - threadIdx.x * 16 + pitch / 2 + (threadIdx.x >> 4) * 4) : "memory");
     }
     __device__ __forceinline__ void load(const int8_t* codes_row, const float* scales_row, int c0, int d, int lane) {
         const int c = c0 + lane * 8;

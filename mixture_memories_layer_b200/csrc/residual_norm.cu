@@ -291,7 +291,7 @@ template <typename XT, typename T, typename G, bool VEC, int C, bool HAS_Y, bool
 // CTAs (warps, with one warp a row) walk the rows.  `red` alternates between
 // two rows, so that one barrier a sum is enough.
 template <typename XT, typename T, bool VEC, int C, bool HAS_Y, int SRC, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : SRC != RING ? 2 : HAS_Y ? 3 : 4)
+__global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : SRC == RING && !HAS_Y ? 4 : 2)
 residual_norm_kernel(const ResNormArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ __align__(16) float red[2][2][kMaxWarps];
@@ -608,10 +608,11 @@ Shape shape_for(int d) {
     return {C, (int)cdiv(chunks, C)};
 }
 
-// Warps an SM that the registers leave (__launch_bounds__): the forward's ring
-// with up to 8 warps a row needs 80 registers, 64 without a block's output,
-// everything else 128.
-constexpr int kRingWarps = 24, kShortWarps = 32, kWarps = 16;
+// Warps an SM that the registers leave (__launch_bounds__): without a block's
+// output the ring needs 64 with up to 8 warps a row, everything else 128.  (24
+// warps with a block's output, 80 registers, spill: 37 us instead of 35 for
+// 16384 x 1024.)
+constexpr int kShortWarps = 32, kWarps = 16;
 constexpr int kSmemSM = 220 * 1024;
 
 template <typename XT, typename T, bool VEC, int C, bool HAS_Y, int MAXT>
@@ -620,11 +621,11 @@ cudaError_t run_fwd(ResNormArgs a, cudaStream_t st) {
     auto* kernel = residual_norm_kernel<XT, T, VEC, C, HAS_Y, SRC, MAXT>;
     const int W = shape_for(a.d).warps, threads = W == 1 ? 128 : 32 * W;
     a.warps_per_row = W;
-    const int ctas = (SRC != RING || MAXT > 256 ? kWarps : HAS_Y ? kRingWarps : kShortWarps) / (threads / 32);
+    const int ctas = (SRC == RING && !HAS_Y && MAXT <= 256 ? kShortWarps : kWarps) / (threads / 32);
     size_t smem = 0;
     if (SRC == RING) {
         typedef Rows<XT, T, T, VEC, C, HAS_Y, false, SRC> R;
-        // at most 24 warps x 6 pieces x 3 slots: 216 KB an SM
+        // at most 16 warps x 6 pieces x 3 slots, or 32 x 2 x 5: 160 KB an SM
         smem = (size_t)R::SLOTS * R::pieces(a) * threads * 16;
         static unsigned long long optin_done = 0;
         const cudaError_t e = smem_optin((const void*)kernel, kSmemSM, &optin_done);

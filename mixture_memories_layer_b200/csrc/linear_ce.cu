@@ -124,6 +124,11 @@ __device__ __forceinline__ float bf16_part(float v, int p) {
     return v;
 }
 
+// The launches of one call follow each other with programmatic stream
+// serialization: a kernel's launch and prologue overlap the end of the one
+// before, and everything that touches memory comes after this.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------- CTA pairs --
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -340,7 +345,6 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
         mbar_init(done_bar, 1);
         *abort_flag = 0;
         fence_barrier_init();
-        if (EPI == EPI_STATS && p.ticket && blockIdx.x == 0) *p.ticket = 0;
     }
     if (warp == 1) pair_tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tc_fence_before();
@@ -348,6 +352,8 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
     cluster_sync();                                // the other CTA's barriers are ready
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    after_previous();
+    if (EPI == EPI_STATS && p.ticket && blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
     const Schedule S(p, EPI);
     Tile T;
 
@@ -642,31 +648,43 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
 }
 
 // ------------------------------------------------------------ small kernels
-// The sum of a product's slots, in order, as its rows of the output: a warp
-// for 32 rows x 32 columns.
+// The sum of a product's slots, in order, as its rows of the output: a block
+// for 32 rows x 32 columns, 8 columns a warp, four slots in flight.
 template <typename T>
-__global__ void __launch_bounds__(256) join_kernel(const Prod q, const int32_t* live, int d, int vec) {
-    __shared__ __align__(16) unsigned char stage[8][PIECE];
+__global__ void __launch_bounds__(128) join_kernel(const Prod q, const int32_t* live, int d) {
+    __shared__ float tile[32][33];
+    after_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t rows = live ? *live : q.rows, cb = cdiv(d, 32), total = cdiv(rows, 32) * cb;
-    for (int64_t u = (int64_t)blockIdx.x * 8 + warp; u < total; u += (int64_t)gridDim.x * 8) {
-        const int64_t rb = u / cb, col = (u - rb * cb) * 32, row = rb * 32 + lane;
-        float v[32], f = 1.f;
-        int64_t to = -1;
-        if (row < rows) {
-            to = q.row_of ? q.row_of[row] : q.row0 + row;
-            f = q.scale ? *q.scale : 1.f;
+    const float f = q.scale ? *q.scale : 1.f;
+    for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
+        const int64_t rb = u / cb, col = (u - rb * cb) * 32;
+        const int64_t stride = partial_at(q, d, 1, 0, 0) - q.partial;
+        const float* at = partial_at(q, d, 0, rb, col + 8 * warp) + lane;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < q.slots; s += 4) {
+            float w[4][8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[k][i] = s + k < q.slots ? at[(s + k) * stride + i * 32] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] += w[k][i];
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        for (int s = 0; s < q.slots; ++s) {
-            const float* at = partial_at(q, d, s, rb, col) + lane;
+        for (int i = 0; i < 8; ++i) tile[lane][8 * warp + i] = v[i] * f;
+        __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += at[i * 32];
+        for (int i = 0; i < 8; ++i) {
+            const int64_t row = rb * 32 + 8 * warp + i;
+            if (row < rows && col + lane < d) {
+                const int64_t to = q.row_of ? q.row_of[row] : q.row0 + row;
+                reinterpret_cast<T*>(q.out)[to * d + col + lane] = from_f<T>(tile[8 * warp + i][lane]);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= f;
-        emit(reinterpret_cast<T*>(q.out), d, vec != 0, to, col, v, smem_u32(stage[warp]), lane);
+        __syncthreads();
     }
 }
 
@@ -688,15 +706,21 @@ __global__ void __launch_bounds__(1024) logsumexp_kernel(const float2* partials,
     __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = (int64_t)blockIdx.x * 32 + lane;
-    float m = -INFINITY, s = 0.f;
+    float m = -INFINITY, s = 0.f, z = 0.f;
+    int64_t tg = -1;
+    after_previous();
     if (row < rows) {
-        for (int q = warp; q < n_part; q += 32 * 4) {
-            float2 v[4];
+        if (warp == 0) {
+            tg = targets[row];
+            if (tg >= 0 && tg < vocab) z = zt[row];
+        }
+        for (int q = warp; q < n_part; q += 32 * 8) {
+            float2 v[8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 8; ++u)
                 v[u] = q + 32 * u < n_part ? partials[(int64_t)(q + 32 * u) * rows + row] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) lse_join(m, s, v[u].x, v[u].y);
+            for (int u = 0; u < 8; ++u) lse_join(m, s, v[u].x, v[u].y);
         }
     }
     sh[warp][lane] = make_float2(m, s);
@@ -724,10 +748,9 @@ __global__ void __launch_bounds__(1024) logsumexp_kernel(const float2* partials,
         float l = 0.f, n = 0.f;
         if (row < rows) {
             const float ls = m + log2f(s) * kLn2;
-            const int64_t tg = targets[row];
             if (tg >= vocab) record_error(ws, MOM_DEVERR_TARGET, row0 + row);
             if (tg >= 0 && tg < vocab) {
-                l = ls - zt[row];
+                l = ls - z;
                 n = 1.f;
             }
             lse[row] = ls;
@@ -765,26 +788,44 @@ __global__ void __launch_bounds__(1024) logsumexp_kernel(const float2* partials,
     }
 }
 
-// A row of d elements as its bf16 parts (each `part` elements after
-// the one before) by one warp.  `vec`: both rows take 16-byte accesses.
+// A row of d elements as its bf16 parts (each `part` elements after the one
+// before) by one warp, several loads in flight.  `vec`: both rows take 16-byte
+// accesses (bf16).
 template <typename T, int PARTS>
-__device__ __forceinline__ void copy_row(const T* src, int d, bf16* dst, int64_t part, bool vec, int lane) {
+__device__ __forceinline__ void copy_row(const T* __restrict__ src, int d, bf16* __restrict__ dst, int64_t part, bool vec,
+                                         int lane) {
     if (PARTS == 1 && vec) {
-        for (int c = lane * 8; c < d; c += 256) {
-            float v[8];
-            load_vec<8>(src + c, v);
-            store_vec<8>(dst + c, v);
+        for (int c0 = lane * 8; c0 < d; c0 += 1024) {
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c0 + 256 * k < d) v[k] = *reinterpret_cast<const uint4*>(src + c0 + 256 * k);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c0 + 256 * k < d) *reinterpret_cast<uint4*>(dst + c0 + 256 * k) = v[k];
         }
         return;
     }
-    for (int c = lane * 2; c < d; c += 64) {       // (pairs stay inside the pitch, which is even)
-        float v[2] = {to_f(src[c]), c + 1 < d ? to_f(src[c + 1]) : 0.f};
+    constexpr int U = 8;
+    for (int c0 = lane * 2; c0 < d; c0 += 64 * U) {      // (pairs stay inside the pitch, which is even)
+        float v[U][2];
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[0], v[1]);
-            *reinterpret_cast<__nv_bfloat162*>(dst + q * part + c) = b;
-            v[0] -= __bfloat162float(b.x);
-            v[1] -= __bfloat162float(b.y);
+        for (int k = 0; k < U; ++k) {
+            const int c = c0 + 64 * k;
+            v[k][0] = c < d ? to_f(src[c]) : 0.f;
+            v[k][1] = c + 1 < d ? to_f(src[c + 1]) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int c = c0 + 64 * k;
+            if (c >= d) break;
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[k][0], v[k][1]);
+                *reinterpret_cast<__nv_bfloat162*>(dst + q * part + c) = b;
+                v[k][0] -= __bfloat162float(b.x);
+                v[k][1] -= __bfloat162float(b.y);
+            }
         }
     }
 }
@@ -793,15 +834,16 @@ __device__ __forceinline__ void copy_row(const T* src, int d, bf16* dst, int64_t
 // (a pitch that is a multiple of 8), float32 split into its three parts.
 template <typename T, int PARTS>
 __global__ void __launch_bounds__(256) parts_kernel(const T* src, int64_t rows, int d, int pitch, bf16* dst) {
+    after_previous();
     const int64_t step = (int64_t)gridDim.x * 8;
     for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += step)
         copy_row<T, PARTS>(src + r * d, d, dst + r * pitch, rows * pitch, false, threadIdx.x & 31);
 }
 
-// The rows that have a target, packed in order.  A block takes 64 rows; it
-// counts the targets before them itself (kCountRows at most; where there are
-// more, count_kernel has counted whole chunks of kCountRows).
-constexpr int kGatherRows = 64, kCountRows = 32768;
+// The rows that have a target, packed in order.  A block takes 8 rows, one a
+// warp; it counts the targets before them itself (kCountRows at most; where
+// there are more, count_kernel has counted whole chunks of kCountRows).
+constexpr int kGatherRows = 8, kCountRows = 16384;
 struct GatherArgs {
     const void* x;
     const int32_t* targets;
@@ -829,6 +871,7 @@ __device__ __forceinline__ int block_sum(int v) {
     return s;
 }
 __global__ void __launch_bounds__(256) count_kernel(const int32_t* targets, int64_t n, int64_t vocab, int32_t* counts) {
+    after_previous();
     const int64_t r0 = (int64_t)blockIdx.x * kCountRows, r1 = r0 + kCountRows < n ? r0 + kCountRows : n;
     int v = 0;
     for (int64_t r = r0 + threadIdx.x; r < r1; r += 256) v += has_target(targets[r], vocab);
@@ -837,44 +880,38 @@ __global__ void __launch_bounds__(256) count_kernel(const int32_t* targets, int6
 }
 template <typename T, int PARTS>
 __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
-    __shared__ int place[kGatherRows];
+    after_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t r0 = (int64_t)blockIdx.x * kGatherRows, chunk = r0 / kCountRows;
+    const int64_t r0 = (int64_t)blockIdx.x * kGatherRows, chunk = r0 / kCountRows, row = r0 + warp;
     int before = 0;
     for (int64_t i = threadIdx.x; i < chunk; i += 256) before += a.counts[i];
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t r = chunk * kCountRows + threadIdx.x; r < r0; r += 256) before += has_target(a.targets[r], a.vocab);
+    const int32_t mine = lane < kGatherRows && r0 + lane < a.n ? a.targets[r0 + lane] : -1;
+    const uint32_t in = __ballot_sync(0xffffffffu, has_target(mine, a.vocab));
     before = block_sum(before);
-    int live = before;
-#pragma unroll
-    for (int h = 0; h < kGatherRows; h += 32) {
-        const bool in = r0 + h + lane < a.n && has_target(a.targets[r0 + h + lane], a.vocab);
-        const uint32_t m = __ballot_sync(0xffffffffu, in);
-        if (warp == 0) place[h + lane] = in ? live + __popc(m & ((1u << lane) - 1)) : -1;
-        live += __popc(m);
-    }
-    __syncthreads();
-    for (int i = warp; i < kGatherRows && r0 + i < a.n; i += 8) {
-        const int64_t row = r0 + i, to = place[i];
-        if (to < 0) {                              // dx of padding is 0
+    const int64_t to = before + __popc(in & ((1u << warp) - 1u));
+    if (row < a.n) {
+        if (!((in >> warp) & 1u)) {                // dx of padding is 0
             T* o = reinterpret_cast<T*>(a.dx) + row * a.d;
             const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (a.vec) for (int c = lane * 8; c < a.d; c += 256) store_vec<8>(o + c, z);
             else for (int c = lane; c < a.d; c += 32) o[c] = from_f<T>(0.f);
-            continue;
-        }
-        const T* x = reinterpret_cast<const T*>(a.x) + row * a.d;
-        copy_row<T, PARTS>(x, a.d, a.xc + to * a.pitch, a.part, a.vec != 0, lane);
-        if (lane == 0) {
-            a.targets_c[to] = a.targets[row];
-            a.row_of[to] = (int32_t)row;
-            a.lse2[to] = a.lse[row] * kLog2e;
-            if (a.dloss) a.weight[to] = a.dloss[row];
+        } else {
+            if (lane == 0) {
+                a.targets_c[to] = a.targets[row];
+                a.row_of[to] = (int32_t)row;
+                a.lse2[to] = a.lse[row] * kLog2e;
+                if (a.dloss) a.weight[to] = a.dloss[row];
+            }
+            copy_row<T, PARTS>(reinterpret_cast<const T*>(a.x) + row * a.d, a.d, a.xc + to * a.pitch, a.part, a.vec != 0,
+                               lane);
         }
     }
     if (r0 + kGatherRows < a.n) return;
     // the last block: the number of rows, and zeros up to whole K blocks of dW
-    if (threadIdx.x == 0) *a.live = live;
+    const int64_t live = before + __popc(in);
+    if (threadIdx.x == 0) *a.live = (int32_t)live;
     for (int64_t r = live + warp; r < cdiv(live, BK) * BK; r += 8)
         for (int q = 0; q < PARTS; ++q)
             for (int c = lane * 2; c < a.d; c += 64)
@@ -955,17 +992,32 @@ Plan plan_for(int64_t n, int d, int64_t v, int dt, bool bwd) {
     return L;
 }
 
+// A launch that follows another one of the same call (`next`) may begin before that one's end.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), int64_t blocks, int threads, size_t smem, bool next, cudaStream_t st, const A&... args) {
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = next ? 1 : 0;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int PARTS, int EPI>
 cudaError_t run_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2, const CUtensorMap& b2,
-                     const GemmArgs& p, int64_t tiles, cudaStream_t st) {
+                     const GemmArgs& p, int64_t tiles, bool next, cudaStream_t st) {
     static unsigned long long optin_done = 0;
     auto* k = ce_gemm_kernel<PARTS, EPI>;
     const cudaError_t e = smem_optin((const void*)k, (int)smem_bytes<PARTS>(), &optin_done);
     if (e != cudaSuccess) return e;
     const int64_t clusters = sm_count() / 2;
-    k<<<(unsigned)(2 * (tiles < clusters ? tiles : clusters)), THREADS, smem_bytes<PARTS>(), st>>>(a, b, a2, b2, p);
-    count_launches(1);
-    return cudaGetLastError();
+    return launch(k, 2 * (tiles < clusters ? tiles : clusters), THREADS, smem_bytes<PARTS>(), next, st, a, b, a2, b2, p);
 }
 
 unsigned warps_grid(int64_t warps) {
@@ -973,12 +1025,16 @@ unsigned warps_grid(int64_t warps) {
     return (unsigned)(b < most ? b : most);
 }
 
-cudaError_t to_parts(const void* src, int dt, int64_t rows, int d, int pitch, void* dst, cudaStream_t st) {
+cudaError_t to_parts(const void* src, int dt, int64_t rows, int d, int pitch, void* dst, bool next, cudaStream_t st) {
     bf16* o = reinterpret_cast<bf16*>(dst);
-    if (dt == MOM_BF16) parts_kernel<bf16, 1><<<warps_grid(rows), 256, 0, st>>>(reinterpret_cast<const bf16*>(src), rows, d, pitch, o);
-    else parts_kernel<float, 3><<<warps_grid(rows), 256, 0, st>>>(reinterpret_cast<const float*>(src), rows, d, pitch, o);
-    count_launches(1);
-    return cudaGetLastError();
+    if (dt == MOM_BF16)
+        return launch(parts_kernel<bf16, 1>, warps_grid(rows), 256, 0, next, st, reinterpret_cast<const bf16*>(src), rows, d, pitch, o);
+    return launch(parts_kernel<float, 3>, warps_grid(rows), 256, 0, next, st, reinterpret_cast<const float*>(src), rows, d, pitch, o);
+}
+
+int64_t join_grid(int64_t rows, int d) {
+    const int64_t b = cdiv(rows, 32) * cdiv(d, 32), most = (int64_t)sm_count() * 16;
+    return b < most ? b : most;
 }
 
 // the piece of W from class v0 on as a TMA operand: in place, or copied
@@ -987,7 +1043,7 @@ struct WPiece {
     uint64_t rows, pitch;
     int row0;
 };
-cudaError_t w_piece(const LinearCeArgs& a, const Plan& L, int64_t v0, int64_t pw, WPiece& w, cudaStream_t st) {
+cudaError_t w_piece(const LinearCeArgs& a, const Plan& L, int64_t v0, int64_t pw, WPiece& w, bool next, cudaStream_t st) {
     if (L.direct) {
         w = WPiece{a.w, (uint64_t)a.v, (uint64_t)a.d, (int)v0};
         return cudaSuccess;
@@ -995,7 +1051,7 @@ cudaError_t w_piece(const LinearCeArgs& a, const Plan& L, int64_t v0, int64_t pw
     char* buf = reinterpret_cast<char*>(a.ws) + L.wbuf;
     w = WPiece{buf, (uint64_t)pw, (uint64_t)L.pitch, 0};
     const size_t es = a.dt == MOM_BF16 ? 2 : 4;
-    return to_parts(reinterpret_cast<const char*>(a.w) + (size_t)v0 * a.d * es, a.dt, pw, a.d, L.pitch, buf, st);
+    return to_parts(reinterpret_cast<const char*>(a.w) + (size_t)v0 * a.d * es, a.dt, pw, a.d, L.pitch, buf, next, st);
 }
 
 #define MOM_TRY(x) do { const cudaError_t e_ = (x); if (e_ != cudaSuccess) return e_; } while (0)
@@ -1004,7 +1060,7 @@ cudaError_t w_piece(const LinearCeArgs& a, const Plan& L, int64_t v0, int64_t pw
 template <int PARTS> cudaError_t fwd(const LinearCeArgs& a, cudaStream_t st) {
     const Plan L = plan_for(a.n, a.d, a.v, a.dt, false);
     char* ws = reinterpret_cast<char*>(a.ws);
-    if (!L.direct) MOM_TRY(to_parts(a.x, a.dt, a.n, a.d, L.pitch, ws + L.xbuf, st));
+    if (!L.direct) MOM_TRY(to_parts(a.x, a.dt, a.n, a.d, L.pitch, ws + L.xbuf, false, st));
     const void* xb = L.direct ? a.x : ws + L.xbuf;
     const int n_part = (int)(2 * cdiv(a.v, BN));
     float2* partials = reinterpret_cast<float2*>(ws + L.partials);
@@ -1019,7 +1075,7 @@ template <int PARTS> cudaError_t fwd(const LinearCeArgs& a, cudaStream_t st) {
         for (int64_t v0 = 0; v0 < a.v; v0 += L.direct ? a.v : L.piece) {
             const int64_t pw = L.direct ? a.v : a.v - v0 < L.piece ? a.v - v0 : L.piece;
             WPiece w;
-            MOM_TRY(w_piece(a, L, v0, pw, w, st));
+            MOM_TRY(w_piece(a, L, v0, pw, w, true, st));
             MOM_MAP(make_tma_3d(&mb, w.base, false, a.d, w.rows, PARTS, w.pitch, HM));
             GemmArgs p{};
             p.rows = rows;
@@ -1033,13 +1089,11 @@ template <int PARTS> cudaError_t fwd(const LinearCeArgs& a, cudaStream_t st) {
             p.zt = zt;
             p.ticket = r0 == 0 ? ticket : nullptr;
             p.ws = a.ws;
-            MOM_TRY((run_gemm<PARTS, EPI_STATS>(ma, mb, ma, mb, p, cdiv(rows, BM) * cdiv(pw, BN), st)));
+            MOM_TRY((run_gemm<PARTS, EPI_STATS>(ma, mb, ma, mb, p, cdiv(rows, BM) * cdiv(pw, BN), !L.direct || r0 > 0, st)));
         }
-        logsumexp_kernel<<<(unsigned)cdiv(rows, 32), 1024, 0, st>>>(
-            partials, n_part, rows, r0, zt, a.targets + r0, a.v, a.loss + r0, a.lse + r0,
-            reinterpret_cast<float2*>(ws + L.sums), ticket, cdiv(a.n, 32), a.mean, a.ws);
-        count_launches(1);
-        MOM_TRY(cudaGetLastError());
+        MOM_TRY(launch(logsumexp_kernel, cdiv(rows, 32), 1024, 0, true, st, (const float2*)partials, n_part, rows, r0,
+                       (const float*)zt, a.targets + r0, a.v, a.loss + r0, a.lse + r0,
+                       reinterpret_cast<float2*>(ws + L.sums), ticket, cdiv(a.n, 32), a.mean, a.ws));
     }
     return cudaSuccess;
 }
@@ -1074,13 +1128,9 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         g.dx = a.dx;
         g.vec = a.d % 8 == 0;
         if (a.n > kCountRows) {
-            count_kernel<<<(unsigned)cdiv(a.n, kCountRows), 256, 0, st>>>(a.targets, a.n, a.v, i32(L.counts));
-            count_launches(1);
-            MOM_TRY(cudaGetLastError());
+            MOM_TRY(launch(count_kernel, cdiv(a.n, kCountRows), 256, 0, false, st, a.targets, a.n, a.v, i32(L.counts)));
         }
-        gather_kernel<T, PARTS><<<(unsigned)cdiv(a.n, kGatherRows), 256, 0, st>>>(g);
-        count_launches(1);
-        MOM_TRY(cudaGetLastError());
+        MOM_TRY(launch(gather_kernel<T, PARTS>, cdiv(a.n, kGatherRows), 256, 0, a.n > kCountRows, st, g));
     }
     CUtensorMap mx_k, mx_mn;       // x: K-major rows of the logits; MN-major rows (K = tokens) of dw
     MOM_MAP(make_tma_3d(&mx_k, xc, false, a.d, L.xrows, PARTS, L.pitch, HM));
@@ -1089,7 +1139,7 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
     for (int64_t v0 = 0; v0 < a.v; v0 += L.piece) {
         const int64_t pw = a.v - v0 < L.piece ? a.v - v0 : L.piece;
         WPiece w;
-        MOM_TRY(w_piece(a, L, v0, pw, w, st));
+        MOM_TRY(w_piece(a, L, v0, pw, w, true, st));
         CUtensorMap mw_k, mw_mn, mg_st, mg_k, mg_mn;
         MOM_MAP(make_tma_3d(&mw_k, w.base, false, a.d, w.rows, PARTS, w.pitch, HM));
         MOM_MAP(make_tma_3d(&mw_mn, w.base, false, a.d, w.rows, PARTS, w.pitch, BK));
@@ -1108,7 +1158,7 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         p.lse2 = f32(L.lse2);
         p.weight = a.dloss ? f32(L.weight) : nullptr;
         p.ws = a.ws;
-        MOM_TRY((run_gemm<PARTS, EPI_GRAD>(mx_k, mw_k, mg_st, mw_k, p, mt * cdiv(pw, BN), st)));
+        MOM_TRY((run_gemm<PARTS, EPI_GRAD>(mx_k, mw_k, mg_st, mw_k, p, mt * cdiv(pw, BN), true, st)));
         p.d = a.d;
         p.bn = L.bn;
         p.vec = vec;
@@ -1130,17 +1180,10 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         p.dw.partial = L.dw_partial ? f32(L.dwp) : nullptr;
         p.dw.last = 1;
         const int64_t nt = cdiv(a.d, L.bn), tiles = mt * nt * L.sx + cdiv(pw, BM) * nt * L.sw;
-        MOM_TRY((run_gemm<PARTS, EPI_OUT>(mg_k, mw_mn, mg_mn, mx_mn, p, tiles, st)));
-        if (L.sx > 1 && p.dx.last) {
-            join_kernel<T><<<warps_grid(cdiv(a.n, 32) * cdiv(a.d, 32)), 256, 0, st>>>(p.dx, live, a.d, vec);
-            count_launches(1);
-            MOM_TRY(cudaGetLastError());
-        }
-        if (L.sw > 1) {
-            join_kernel<T><<<warps_grid(cdiv(pw, 32) * cdiv(a.d, 32)), 256, 0, st>>>(p.dw, nullptr, a.d, vec);
-            count_launches(1);
-            MOM_TRY(cudaGetLastError());
-        }
+        MOM_TRY((run_gemm<PARTS, EPI_OUT>(mg_k, mw_mn, mg_mn, mx_mn, p, tiles, true, st)));
+        if (L.sx > 1 && p.dx.last)
+            MOM_TRY(launch(join_kernel<T>, join_grid(a.n, a.d), 128, 0, true, st, p.dx, live, a.d));
+        if (L.sw > 1) MOM_TRY(launch(join_kernel<T>, join_grid(pw, a.d), 128, 0, true, st, p.dw, (const int32_t*)nullptr, a.d));
     }
     return cudaSuccess;
 }

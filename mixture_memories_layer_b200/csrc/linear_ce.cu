@@ -55,14 +55,14 @@ namespace {
 
 using namespace sm100;
 
-constexpr int BM = 256, BN = 256, BK = 64;           // a cluster's tile
+constexpr int BM = 256, BN_MAX = 256, BK = 64;       // a cluster's tile (columns: 256 or 128)
 constexpr int HM = BM / 2;                           // a CTA's rows of A, and of B
 constexpr int OP_BYTES = HM * BK * 2;                // one operand part of a stage
 constexpr int MN_GROUP = 64 * BK * 2;                // an MN-major box: 64 MN x 64 K, bf16
 constexpr int NEPI = 256, THREADS = 64 + NEPI;
 constexpr int EPI_ARRIVE = 2 * NEPI / 32;            // warps of both CTAs that free an accumulator
 constexpr int PIECE = 32 * 128;                      // an epilogue warp's staging: 32 rows x 128 bytes
-constexpr uint32_t TMEM_COLS = 2 * BN;
+constexpr uint32_t TMEM_COLS = 2 * BN_MAX;
 constexpr int SEG_KB = 2;                            // float32: K blocks between two reads of the accumulator
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 template <int PARTS> struct Stages { static constexpr int N = PARTS == 1 ? 6 : 2, BYTES = 2 * PARTS * OP_BYTES; };
@@ -97,7 +97,7 @@ struct GemmArgs {
     int32_t* ticket;                     // STATS: set to 0 for logsumexp_kernel
     // OUT: dx (rows and K of dw follow `live`), dw
     Prod dx, dw;
-    int d, bn, vec;                      // bn: columns of a tile; vec: out's rows take 16-byte stores
+    int d, vec;                          // vec: out's rows take 16-byte stores
     void* ws;
 };
 
@@ -196,19 +196,19 @@ struct Tile {
 struct Schedule {
     int64_t c, n, m1, m2, n_tiles, na, nb, head, first;
     int kb1, kb2, k1, k2, dw_first;
-    __device__ __forceinline__ Schedule(const GemmArgs& p, int epi) {
+    __device__ __forceinline__ Schedule(const GemmArgs& p, int epi, int parts, int bn) {
         c = blockIdx.x >> 1;
         n = gridDim.x >> 1;
         const int64_t live = p.live ? *p.live : p.rows;
         m1 = cdiv(live, BM);
         dw_first = 0;
         if (epi != EPI_OUT) {
-            n_tiles = cdiv(p.cols, BN);
+            n_tiles = cdiv(p.cols, bn);
             na = m1 * n_tiles;
             k1 = p.kb;
             return;
         }
-        n_tiles = cdiv(p.d, p.bn);
+        n_tiles = cdiv(p.d, bn);
         m2 = cdiv(p.dw.rows, BM);
         kb1 = p.dx.kb;
         kb2 = (int)cdiv(live, BK);
@@ -219,8 +219,9 @@ struct Schedule {
         na = dw_first ? n2 : n1;
         nb = dw_first ? n1 : n2;
         first = na % n;                            // clusters that get one more
-        // (an epilogue lasts about 4 K blocks)
-        head = first ? (dw_first ? (k2 + 4) / (k1 + 4) : (k1 + 4) / (k2 + 4)) : 0;
+        // (an epilogue lasts about 4 K blocks, or one of six products each)
+        const int e = parts == 1 ? 4 : 1;
+        head = first ? (dw_first ? (k2 + e) / (k1 + e) : (k1 + e) / (k2 + e)) : 0;
     }
     __device__ __forceinline__ bool at(int epi, int64_t j, Tile& T) const {
         int64_t t = c + j * n;
@@ -313,7 +314,7 @@ __device__ __forceinline__ float* partial_at(const Prod& q, int d, int slot, int
     return q.partial + ((slot * blocks + rb) * dp + col) * 32;
 }
 
-template <int PARTS, int EPI>
+template <int PARTS, int EPI, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                const __grid_constant__ CUtensorMap tm_a2, const __grid_constant__ CUtensorMap tm_b2,
@@ -354,20 +355,20 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
     const uint32_t tmem_base = *tmem_slot;
     after_previous();
     if (EPI == EPI_STATS && p.ticket && blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
-    const Schedule S(p, EPI);
+    const Schedule S(p, EPI, PARTS, BN);
     Tile T;
 
     if (warp == 0) {
         if (lane == 0) {
             // ---------------------------------------------------- TMA loads
             const uint32_t full_lead = leader_addr(full0);
-            const int groups = EPI == EPI_OUT ? p.bn / 128 : 2;
-            const uint32_t stage_tx = 2 * PARTS * (OP_BYTES + (EPI == EPI_OUT ? groups * MN_GROUP : OP_BYTES));
+            constexpr int groups = BN / 128;
+            constexpr uint32_t stage_tx = 2 * PARTS * (OP_BYTES + BN / 2 * BK * 2);
             uint32_t it = 0;
             bool ok = true;
             for (int64_t j = 0; ok && S.at(EPI, j, T); ++j) {
                 const int m0 = (int)(T.mt * BM) + HM * rank;
-                const int n0 = EPI == EPI_OUT ? (int)(T.nt * p.bn + p.bn / 2 * rank) : (int)(T.nt * BN) + HM * (int)rank;
+                const int n0 = (int)(T.nt * BN) + BN / 2 * (int)rank;
                 for (int kb = T.kb0; kb < T.kb1; ++kb, ++it) {
                     const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
                     if (!mbar_wait(empty0 + 8 * s, ph ^ 1, abort_flag, p.ws, 1)) { ok = false; break; }
@@ -402,18 +403,17 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             // --------------------------------------------------- MMA issuer
-            const int bn = EPI == EPI_OUT ? p.bn : BN;
             uint32_t it = 0, tc = 0;
             bool ok = true;
             for (int64_t j = 0; ok && S.at(EPI, j, T); ++j) {
                 const bool a_mn = EPI == EPI_OUT && T.dw;
-                const uint32_t idesc = idesc_bf16_f32(BM, bn, a_mn, EPI == EPI_OUT);
+                const uint32_t idesc = idesc_bf16_f32(BM, BN, a_mn, EPI == EPI_OUT);
                 const int seg = SEG ? SEG_KB : T.kb1 - T.kb0;
                 for (int k0 = T.kb0; ok && k0 < T.kb1; k0 += seg, ++tc) {
                     const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
                     if (!mbar_wait(tempty0 + 8 * acc, aph ^ 1, abort_flag, p.ws, 2)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + acc * BN;
+                    const uint32_t d_tmem = tmem_base + acc * BN_MAX;
                     const int k1 = k0 + seg < T.kb1 ? k0 + seg : T.kb1;
                     for (int kb = k0; kb < k1; ++kb, ++it) {
                         const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
@@ -447,7 +447,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
         // ------------------------------------------------------- epilogue
         // warp 2 + e: TMEM lanes 32 (warp % 4) .. + 31, half e / 4 of the tile's columns
         const int e = warp - 2, qd = warp & 3, hf = e >> 2;
-        const int half = EPI == EPI_OUT ? p.bn / 2 : BN / 2;
+        constexpr int half = BN / 2;
         const uint32_t piece = smem_u32(sOut + e * PIECE);
         const uint32_t lead_tempty = leader_addr(tempty0);
         const int64_t live = p.live ? *p.live : p.rows;
@@ -455,7 +455,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
         bool ok = true;
         for (int64_t j = 0; S.at(EPI, j, T); ++j) {
             const int64_t row = T.mt * BM + HM * rank + 32 * qd + lane;
-            const int64_t col0 = EPI == EPI_OUT ? T.nt * p.bn + hf * half : T.nt * BN + hf * half;
+            const int64_t col0 = T.nt * BN + hf * half;
             int tl = -1;                           // the target's column inside this half tile (< 0: not here)
             float lse2 = 0.f, wt = 1.f;
             if constexpr (EPI != EPI_OUT) {
@@ -469,25 +469,23 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                 }
             }
             // float32: the tile's sum, continued in registers
-            float sum[SEG ? 128 : 1];
+            float sum[SEG ? half : 1];
             uint32_t acc = tc & 1;
             if constexpr (SEG) {
 #pragma unroll
-                for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+                for (int i = 0; i < half; ++i) sum[i] = 0.f;
                 for (int k0 = T.kb0; k0 < T.kb1; k0 += SEG_KB, ++tc) {
                     acc = tc & 1;
                     if (!mbar_wait(tfull0 + 8 * acc, (tc >> 1) & 1, abort_flag, p.ws, 4)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t ta = tmem_base + ((uint32_t)(32 * qd) << 16) + acc * BN + hf * half;
+                    const uint32_t ta = tmem_base + ((uint32_t)(32 * qd) << 16) + acc * BN_MAX + hf * half;
 #pragma unroll
-                    for (int c = 0; c < 128; c += 32) {
-                        if (c < half) {
-                            uint32_t r[32];
-                            tmem_ld_x32(ta + c, r);
-                            tmem_ld_wait();
+                    for (int c = 0; c < half; c += 32) {
+                        uint32_t r[32];
+                        tmem_ld_x32(ta + c, r);
+                        tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(r[i]);
-                        }
+                        for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(r[i]);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -498,7 +496,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                 tc_fence_after();
             }
             if (!ok) break;
-            const uint32_t taddr = tmem_base + ((uint32_t)(32 * qd) << 16) + acc * BN + hf * half;
+            const uint32_t taddr = tmem_base + ((uint32_t)(32 * qd) << 16) + acc * BN_MAX + hf * half;
             // columns c .. c + 31 of the half tile (an empty K range: zeros)
             auto chunk = [&](int c, float* v) {
                 if constexpr (SEG) {
@@ -525,8 +523,8 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                 }
                 const int64_t rb = T.mt * (BM / 32) + (HM / 32) * rank + qd;
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    if (c < half && col0 + c < p.d && rb * 32 < rows) {
+                for (int c = 0; c < half; c += 32) {
+                    if (col0 + c < p.d && rb * 32 < rows) {
                         float v[32];
                         chunk(c, v);
                         if (q.partial) {
@@ -553,7 +551,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                 if constexpr (EPI == EPI_STATS) {
                     float m = -INFINITY, s = 0.f, zt = 0.f;
 #pragma unroll
-                    for (int c = 0; c < 128; c += 32) {
+                    for (int c = 0; c < half; c += 32) {
                         float v[32];
                         chunk(c, v);
                         if (c + 32 > nv) {
@@ -592,7 +590,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
 #pragma unroll
-                        for (int pc = 0; pc < 2; ++pc) {
+                        for (int pc = 0; pc < half / 64; ++pc) {
                             if (lane == 0) bulk_wait_read0();      // the previous piece has left shared memory
                             __syncwarp();
 #pragma unroll
@@ -938,11 +936,21 @@ struct Plan {
     int pitch;             // row pitch of copied operands (elements)
     int64_t piece;         // classes of a piece (a multiple of 256)
     int64_t xrows;         // rows of the packed x
-    int bn;                // columns of an OUT tile
+    int bn, bn_logits;     // columns of a tile: OUT; STATS or GRAD
     int sx, sw;            // K slots of dx and dw
     bool dx_partial, dw_partial;
     size_t zt, partials, sums, ticket, xbuf, wbuf, g, dxp, dwp, targets, row_of, lse2, weight, live, counts, bytes;
 };
+
+// Columns of the logits' tiles, 256, or 128 where the clusters then finish
+// first: by the instructions' cycles (512 for 256 columns of a K block) and
+// 1500 for a tile's rest.  200 tokens of 8000 classes, d 360, float32: 121 us
+// with 256 (32 tiles for 74 clusters), 88 us with 128.
+int columns_for(int64_t rows, int64_t cols, int d, int parts, int clusters) {
+    const int64_t kb = cdiv(d, BK) * (parts == 1 ? 1 : 6), m = cdiv(rows, BM);
+    auto cost = [&](int bn) { return cdiv(m * cdiv(cols, bn), clusters) * (kb * 2 * bn + 1500); };
+    return cost(128) < cost(256) ? 128 : 256;
+}
 
 Plan plan_for(int64_t n, int d, int64_t v, int dt, bool bwd) {
     Plan L{};
@@ -963,17 +971,22 @@ Plan plan_for(int64_t n, int d, int64_t v, int dt, bool bwd) {
     if (!bwd) {
         const int64_t rows = n < kRowChunk ? n : kRowChunk;
         L.zt = take(rows * 4);
-        L.partials = take((size_t)rows * 2 * cdiv(v, BN) * 8);
+        L.bn_logits = columns_for(rows, L.direct ? v : L.piece, d, L.parts, clusters);
+        const int64_t cols = L.direct ? v : L.piece;           // (a copied W comes in pieces)
+        L.partials = take((size_t)rows * 2 * (v / cols * cdiv(cols, L.bn_logits) + cdiv(v % cols, L.bn_logits)) * 8);
         L.sums = take((size_t)cdiv(n, 32) * 8);
         L.ticket = take(4);
     } else {
-        L.bn = d <= 128 ? 128 : BN;
-        // K blocks of a tile, and of a cluster's share of a piece with each
-        // tile's epilogue counted as 4 of them
+        // 128 columns where 256 would leave a quarter or more of them empty
+        L.bn = d <= 128 || (d > 256 && d <= 384) ? 128 : 256;
+        L.bn_logits = columns_for(n, L.piece < v ? L.piece : v, d, L.parts, clusters);
+        // K blocks of a tile, and of a cluster's share of a piece, each tile's
+        // epilogue counted as 4 of them (float32, six products a block: as 1)
         const int64_t nt = cdiv(d, L.bn), k1 = cdiv(v < L.piece ? v : L.piece, BK), k2 = cdiv(n, BK);
         const int64_t t1 = cdiv(n, BM) * nt, t2 = cdiv(L.piece, BM) * nt;
-        int64_t share = cdiv(t1 * (k1 + 4) + t2 * (k2 + 4), clusters);
-        if (share < 16) share = 16;
+        const int64_t e = b16 ? 4 : 1;
+        int64_t share = cdiv(t1 * (k1 + e) + t2 * (k2 + e), clusters);
+        if (share < 4 * e) share = 4 * e;
         L.sx = (int)cdiv(k1, share);
         L.sw = (int)cdiv(k2, share);
         L.dx_partial = L.sx > 1 || L.piece < v;
@@ -1009,15 +1022,21 @@ cudaError_t launch(void (*kernel)(P...), int64_t blocks, int threads, size_t sme
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int PARTS, int EPI>
-cudaError_t run_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2, const CUtensorMap& b2,
-                     const GemmArgs& p, int64_t tiles, bool next, cudaStream_t st) {
+template <int PARTS, int EPI, int BN>
+cudaError_t run_tiles(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2, const CUtensorMap& b2,
+                      const GemmArgs& p, int64_t tiles, bool next, cudaStream_t st) {
     static unsigned long long optin_done = 0;
-    auto* k = ce_gemm_kernel<PARTS, EPI>;
+    auto* k = ce_gemm_kernel<PARTS, EPI, BN>;
     const cudaError_t e = smem_optin((const void*)k, (int)smem_bytes<PARTS>(), &optin_done);
     if (e != cudaSuccess) return e;
     const int64_t clusters = sm_count() / 2;
     return launch(k, 2 * (tiles < clusters ? tiles : clusters), THREADS, smem_bytes<PARTS>(), next, st, a, b, a2, b2, p);
+}
+template <int PARTS, int EPI>
+cudaError_t run_gemm(int bn, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2, const CUtensorMap& b2,
+                     const GemmArgs& p, int64_t tiles, bool next, cudaStream_t st) {
+    return bn == 128 ? run_tiles<PARTS, EPI, 128>(a, b, a2, b2, p, tiles, next, st)
+                     : run_tiles<PARTS, EPI, 256>(a, b, a2, b2, p, tiles, next, st);
 }
 
 unsigned warps_grid(int64_t warps) {
@@ -1062,12 +1081,13 @@ template <int PARTS> cudaError_t fwd(const LinearCeArgs& a, cudaStream_t st) {
     char* ws = reinterpret_cast<char*>(a.ws);
     if (!L.direct) MOM_TRY(to_parts(a.x, a.dt, a.n, a.d, L.pitch, ws + L.xbuf, false, st));
     const void* xb = L.direct ? a.x : ws + L.xbuf;
-    const int n_part = (int)(2 * cdiv(a.v, BN));
+    int n_part = 0;
     float2* partials = reinterpret_cast<float2*>(ws + L.partials);
     float* zt = reinterpret_cast<float*>(ws + L.zt);
     int32_t* ticket = reinterpret_cast<int32_t*>(ws + L.ticket);
     for (int64_t r0 = 0; r0 < a.n; r0 += kRowChunk) {
         const int64_t rows = a.n - r0 < kRowChunk ? a.n - r0 : kRowChunk;
+        n_part = 0;
         CUtensorMap ma, mb;
         // the chunk's rows: a map that starts at r0; the parts lie n rows apart
         MOM_MAP(make_tma_3d(&ma, reinterpret_cast<const bf16*>(xb) + r0 * L.pitch, false, a.d, rows, PARTS, L.pitch,
@@ -1076,7 +1096,7 @@ template <int PARTS> cudaError_t fwd(const LinearCeArgs& a, cudaStream_t st) {
             const int64_t pw = L.direct ? a.v : a.v - v0 < L.piece ? a.v - v0 : L.piece;
             WPiece w;
             MOM_TRY(w_piece(a, L, v0, pw, w, true, st));
-            MOM_MAP(make_tma_3d(&mb, w.base, false, a.d, w.rows, PARTS, w.pitch, HM));
+            MOM_MAP(make_tma_3d(&mb, w.base, false, a.d, w.rows, PARTS, w.pitch, L.bn_logits / 2));
             GemmArgs p{};
             p.rows = rows;
             p.cols = pw;
@@ -1085,11 +1105,12 @@ template <int PARTS> cudaError_t fwd(const LinearCeArgs& a, cudaStream_t st) {
             p.targets = a.targets + r0;
             p.v0 = v0;
             p.vocab = a.v;
-            p.partials = partials + v0 / BN * 2 * rows;
+            p.partials = partials + n_part * rows;
+            n_part += (int)(2 * cdiv(pw, L.bn_logits));
             p.zt = zt;
             p.ticket = r0 == 0 ? ticket : nullptr;
             p.ws = a.ws;
-            MOM_TRY((run_gemm<PARTS, EPI_STATS>(ma, mb, ma, mb, p, cdiv(rows, BM) * cdiv(pw, BN), !L.direct || r0 > 0, st)));
+            MOM_TRY((run_gemm<PARTS, EPI_STATS>(L.bn_logits, ma, mb, ma, mb, p, cdiv(rows, BM) * cdiv(pw, L.bn_logits), !L.direct || r0 > 0, st)));
         }
         MOM_TRY(launch(logsumexp_kernel, cdiv(rows, 32), 1024, 0, true, st, (const float2*)partials, n_part, rows, r0,
                        (const float*)zt, a.targets + r0, a.v, a.loss + r0, a.lse + r0,
@@ -1141,7 +1162,7 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         WPiece w;
         MOM_TRY(w_piece(a, L, v0, pw, w, true, st));
         CUtensorMap mw_k, mw_mn, mg_st, mg_k, mg_mn;
-        MOM_MAP(make_tma_3d(&mw_k, w.base, false, a.d, w.rows, PARTS, w.pitch, HM));
+        MOM_MAP(make_tma_3d(&mw_k, w.base, false, a.d, w.rows, PARTS, w.pitch, L.bn_logits / 2));
         MOM_MAP(make_tma_3d(&mw_mn, w.base, false, a.d, w.rows, PARTS, w.pitch, BK));
         MOM_MAP(make_tma_3d(&mg_st, ws + L.g, false, L.piece, L.xrows, PARTS, L.piece, 32));
         MOM_MAP(make_tma_3d(&mg_k, ws + L.g, false, L.piece, L.xrows, PARTS, L.piece, HM));
@@ -1158,9 +1179,8 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         p.lse2 = f32(L.lse2);
         p.weight = a.dloss ? f32(L.weight) : nullptr;
         p.ws = a.ws;
-        MOM_TRY((run_gemm<PARTS, EPI_GRAD>(mx_k, mw_k, mg_st, mw_k, p, mt * cdiv(pw, BN), true, st)));
+        MOM_TRY((run_gemm<PARTS, EPI_GRAD>(L.bn_logits, mx_k, mw_k, mg_st, mw_k, p, mt * cdiv(pw, L.bn_logits), true, st)));
         p.d = a.d;
-        p.bn = L.bn;
         p.vec = vec;
         p.dx.rows = a.n;
         p.dx.kb = (int)cdiv(pw, BK);
@@ -1180,7 +1200,7 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         p.dw.partial = L.dw_partial ? f32(L.dwp) : nullptr;
         p.dw.last = 1;
         const int64_t nt = cdiv(a.d, L.bn), tiles = mt * nt * L.sx + cdiv(pw, BM) * nt * L.sw;
-        MOM_TRY((run_gemm<PARTS, EPI_OUT>(mg_k, mw_mn, mg_mn, mx_mn, p, tiles, true, st)));
+        MOM_TRY((run_gemm<PARTS, EPI_OUT>(L.bn, mg_k, mw_mn, mg_mn, mx_mn, p, tiles, true, st)));
         if (L.sx > 1 && p.dx.last)
             MOM_TRY(launch(join_kernel<T>, join_grid(a.n, a.d), 128, 0, true, st, p.dx, live, a.d));
         if (L.sw > 1) MOM_TRY(launch(join_kernel<T>, join_grid(pw, a.d), 128, 0, true, st, p.dw, (const int32_t*)nullptr, a.d));

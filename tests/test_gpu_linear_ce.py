@@ -269,3 +269,95 @@ def test_another_stream_and_captured_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(out[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("live", [1, 63, 64, 65, 127, 128, 129, 256, 257, 300])
+def test_rows_with_a_target_at_the_tiles_edges(t, live):
+    """Only rows that have a target take part in the gradient; their number
+    falls on and beside the edges of 64 (K of dw) and 256 (rows of a tile)."""
+    x, w, tg = _problem(300, 72, 333, t, seed=20, pad=0.0)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(live)
+    tg[torch.randperm(300, generator=g, device="cuda")[live:]] = -100
+    _, f, b = _check(x, w, tg, t)
+    assert torch.all(b["dx"][tg < 0] == 0)
+    r = torch.randn(300, generator=g, device="cuda")
+    _check(x, w, tg, t, r)
+
+
+@pytest.mark.parametrize("t,d", [("bf16", 64), ("bf16", 65), ("f32", 64)])
+def test_padding_rows_may_hold_anything(t, d):
+    """NaN and infinities in x and dloss of rows without a target: loss, dx and
+    dw bit for bit as with zeros there."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    x, w, tg = _problem(200, d, 500, t, seed=22, pad=0.5)
+    pad = (tg < 0).nonzero()[:, 0]
+    r = torch.rand(200, device="cuda")
+    x0, x1, r0, r1 = x.clone(), x.clone(), r.clone(), r.clone()
+    x0[pad], r0[pad] = 0, 0
+    x1[pad[::2]], x1[pad[1::2]], r1[pad] = float("nan"), float("inf"), float("nan")
+    outs = []
+    for xx, rr in ((x0, r0), (x1, r1)):
+        head = LMHead(w)
+        f = head.loss(xx, tg)
+        outs.append((f["loss"].clone(), f["mean"].clone(), *[v.clone() for v in head.backward(xx, tg).values()],
+                     *[v.clone() for v in head.backward(xx, tg, rr).values()]))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    assert torch.all(outs[0][2][pad] == 0)
+
+
+@pytest.mark.parametrize("n,d,v,t,pad", [(20000, 64, 700, "bf16", 0.8), (40000, 40, 300, "f32", 0.5), (16385, 72, 257, "bf16", 0.1),
+                                         (12000, 512, 1000, "bf16", 0.0), (4096, 64, 132000, "bf16", 0.3),
+                                         (200, 360, 8000, "f32", 0.1), (3000, 300, 6000, "f32", 0.1)])
+def test_long_batches_and_slots(n, d, v, t, pad):
+    """Rows counted in chunks (n > 16384), token and vocabulary axes split into
+    slots, several pieces with slots, tiles of 128 and 256 columns; by 2-norm,
+    bf16 two roundings of at most 2^-8 each, float32 1e-5 (a logit's float32
+    error in its exponential is the largest)."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    x, w, tg = _problem(n, d, v, t, seed=23, pad=pad)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(2)
+    r = torch.rand(n, generator=gen, device="cuda") + 0.5
+    head = LMHead(w)
+    f, g = head.loss(x, tg), {k: a.clone() for k, a in head.backward(x, tg).items()}
+    h = head.backward(x, tg, r)
+    loss, lse, dx, dw = _torch64(x, w, tg)
+    lim = 2.0 ** -7 if t == "bf16" else 1e-5
+    rel = lambda a, b: float((a.double() - b).norm() / b.norm())
+    assert rel(f["loss"], loss) < 1e-5 and rel(f["lse"], lse) < 1e-5
+    assert rel(g["dx"], dx) < lim and rel(g["dw"], dw) < lim
+    assert torch.all(g["dx"][tg < 0] == 0) and torch.all(h["dx"][tg < 0] == 0)
+    # rows' weights: dx scales by them; dw from the rows' scaled x
+    count = (tg >= 0).sum()
+    assert rel(h["dx"], dx * (r * count).double()[:, None]) < lim
+    z = torch.exp(x.double() @ w.double().t() - lse[:, None])
+    z.scatter_add_(1, tg.long().clamp(min=0)[:, None], -torch.ones_like(lse)[:, None])
+    assert rel(h["dw"], z.t() @ (x.double() * (r * (tg >= 0)).double()[:, None])) < lim
+
+
+def test_gradients_are_differences_of_the_loss():
+    """float32, along random directions: (L(x + e a) - L(x - e a)) / 2e of the
+    mean loss against <dx, a>, the same for w.  Error: the third derivative
+    (e^2 times a constant of the order of the direction's logits cubed, e =
+    2^-8 and logits of about 1: 2^-16 x 8) and the loss's own float32 error,
+    2^-21 x 8 / 2e = 2^-11."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    x, w, tg = _problem(60, 48, 200, "f32", seed=24, std=1.0)
+    head = LMHead(w)
+    head.loss(x, tg)
+    grads = {k: v.double().clone() for k, v in head.backward(x, tg).items()}
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(4)
+    e = 2.0 ** -8
+    for name, t in (("dx", x), ("dw", w)):
+        for _ in range(4):
+            a = torch.randn(t.shape, generator=gen, device="cuda") / 48 ** 0.5
+            out = []
+            for s in (e, -e):
+                xx, ww = (x + s * a, w) if name == "dx" else (x, w + s * a)
+                loss = LMHead(ww.contiguous()).loss(xx.contiguous(), tg)["loss"].double()
+                out.append(loss.sum() / (tg >= 0).sum())
+            got, want = float((out[0] - out[1]) / (2 * e)), float((grads[name] * a).sum())
+            assert abs(got - want) < 2.0 ** -11 + 2.0 ** -13, (name, got, want)

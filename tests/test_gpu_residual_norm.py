@@ -341,3 +341,76 @@ def test_another_stream_and_a_captured_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o[k], want[k]) for k in want)
+
+
+# more rows than the GPU holds at once: every CTA walks several, the copies
+# ahead of it wrap around their slots
+MANY = [(20000, 200, "bf16", "bf16"), (12001, 256, "q8", "f32"), (4003, 1024, "f32", "f32"), (1701, 2048, "q8", "bf16"),
+        (901, 4000, "bf16", "bf16"), (401, 8192, "f32", "bf16"), (310, 9000, "q8", "bf16"), (3001, 1021, "f32", "bf16"),
+        (905, 3001, "bf16", "bf16"), (403, 7777, "f32", "f32")]
+
+
+@pytest.mark.parametrize("n,d,x,t", MANY)
+def test_many_rows_forward(n, d, x, t):
+    test_forward_against_fp64(n, d, x, t, "token" if n % 2 else "elem")
+
+
+@pytest.mark.parametrize("n,d,x,t", MANY)
+def test_many_rows_backward(n, d, x, t):
+    test_backward_against_fp64(n, d, x, t, "f32", "token" if n % 2 else "elem", n % 4 != 1)
+
+
+@pytest.mark.parametrize("n,d,dt", [(9001, 1024, "bf16"), (40001, 256, "f32"), (2003, 8200, "bf16"), (3001, 1001, "f32")])
+def test_many_rows_restore_and_norm(n, d, dt):
+    """The checkpoint of many rows, restored with its norm: the stream bit for
+    bit as mom_act_unpack8 restores it."""
+    from mixture_memories_layer_b200 import binding as B
+    p, _ = _inputs(n, d, dt, dt, "none", scale=False, y=False, seed=21)
+    k8 = B.new_act8(n, d)
+    B.mom_act_pack8(p["x"], k8)
+    codes, scales = T.act8_pack(_np(p["x"]).astype(np.float32))
+    assert np.array_equal(k8[0].cpu().numpy(), codes) and np.array_equal(k8[1].cpu().numpy(), scales)
+    x_hat, x_out, h = torch.empty_like(p["x"]), torch.empty_like(p["x"]), torch.empty_like(p["x"])
+    B.mom_act_unpack8(k8, x_hat)
+    B.mom_residual_norm(k8, None, None, None, None, p["w_pre"], EPS, x_out, h)
+    assert torch.equal(x_hat, x_out)
+    x32 = torch.empty((n, d), device="cuda")
+    B.mom_act_unpack8(k8, x32)
+    _, hh = T.residual_norm(x=_np(x32), y=None, gate=None, w_post=None, res_scale=None, w_pre=_np(p["w_pre"]), eps=EPS)
+    r = np.abs(hh)
+    _close(h, hh, r)
+
+
+def test_gates_at_their_ends():
+    """Gates of +-infinity, large and small logits: exactly 0 or the whole
+    block, and a gradient that does not cancel (1 - sigma = e^-z / (1 + e^-z)
+    for z > 0)."""
+    from mixture_memories_layer_b200 import binding as B
+    n, d = 12, 512
+    p, x64 = _inputs(n, d, "f32", "f32", "token", seed=31)
+    z = torch.tensor([float("inf"), float("-inf"), 200.0, -200.0, 80.0, -80.0, 30.0, -30.0, 15.0, -15.0, 8.0, 0.0],
+                     device="cuda").view(n, 1)
+    for gate in (z, z.expand(n, d).contiguous()):
+        q = dict(p, gate=gate)
+        x_out, h = torch.empty_like(p["x"]), torch.empty_like(p["x"])
+        B.mom_residual_norm(**q, eps=EPS, x_out=x_out, h=h)
+        whole, none = torch.empty_like(x_out), torch.empty_like(h)
+        B.mom_residual_norm(**dict(q, gate=None), eps=EPS, x_out=whole, h=none)
+        assert torch.equal(x_out[0], whole[0]) and torch.equal(x_out[1], p["x"][1])
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(5)
+        dx_out = torch.randn((n, d), generator=gen, device="cuda")
+        dh = torch.randn((n, d), generator=gen, device="cuda")
+        got = _backward(q, dx_out, dh, torch.float32)
+        assert torch.all(got["dgate"][:2] == 0)
+        # |z| <= 15, where float64 forms 1 - sigma to 2^-30: the error stays
+        # relative to sigma (1 - sigma).  The exponential adds two ulps and its
+        # argument's rounding, |z| 2^-24 relative, to the 2^-17 above; a token's
+        # gate is a sum over the row.
+        mid = slice(8, 12)
+        ref = T.residual_norm_bwd(**dict(_ref(q, x64), gate=_np(gate.clamp(-300, 300))), eps=EPS, dx_out=_np(dx_out),
+                                  dh=_np(dh))
+        zz = _np(z)[mid]
+        size = ref["size"]["dgate"][mid] / (1 + np.exp(zz))
+        lim = (F32 + 2.0 ** -22 + np.abs(zz) * 2.0 ** -23 + d * 2.0 ** -24 / 32) * size
+        assert np.all(np.abs(_np(got["dgate"])[mid] - ref["dgate"][mid]) <= lim)

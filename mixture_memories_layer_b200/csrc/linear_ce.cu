@@ -93,6 +93,8 @@ struct GemmArgs {
     int64_t v0, vocab;                   // the piece's first class
     float2* partials;                    // [column half tiles][rows]
     float* zt;                           // the targets' logits
+    bf16* g;                             // GRAD: [parts][.., g_pitch], the parts g_part elements apart
+    int64_t g_pitch, g_part;
     const float *lse2, *weight;          // GRAD: log2(e) lse of the packed rows, their weights (null: 1)
     int32_t* ticket;                     // STATS: set to 0 for logsumexp_kernel
     // OUT: dx (rows and K of dw follow `live`), dw
@@ -106,11 +108,6 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
-                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1), "r"(c2)
-                 : "memory");
-}
 __device__ __forceinline__ void st_shared_v4(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -118,16 +115,20 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&h);
 }
-// part p of the exact split of v into bf16 parts
-__device__ __forceinline__ float bf16_part(float v, int p) {
-    for (int i = 0; i < p; ++i) v -= __bfloat162float(__float2bfloat16_rn(v));
-    return v;
+// one 32-byte sector
+__device__ __forceinline__ void st_global_32(bf16* dst, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 // The launches of one call follow each other with programmatic stream
 // serialization: a kernel's launch and prologue overlap the end of the one
-// before, and everything that touches memory comes after this.
-__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// before, and everything that touches memory comes after this (TMA reads what
+// that kernel wrote by plain stores, hence the fence).
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;\n\tfence.proxy.async.global;" ::: "memory");
+}
 
 // ------------------------------------------------------- CTA pairs --
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -584,38 +585,36 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                         if (tl >= 0) p.zt[row] = zt;
                     }
                 } else {
-                    // g is 0 past the vocabulary and past the packed rows
+                    // g is 0 past the vocabulary and past the packed rows, up to whole
+                    // K blocks of dW.  A lane writes its row in 32-byte sectors, past
+                    // shared memory: the MMAs' operands and the copies that bring them
+                    // take all of its bandwidth.
                     const int nvr = row < live ? nv : 0;
-                    const bool some = T.mt * BM + HM * rank + 32 * qd < cdiv(live, BK) * BK;   // whole K blocks of dW
+                    bf16* out = p.g + row * p.g_pitch + col0;
+                    const bool some = row < cdiv(live, BK) * BK;
 #pragma unroll
-                    for (int part = 0; part < PARTS; ++part) {
+                    for (int c = 0; c < half; c += 32) {
+                        float g[32];
+                        chunk(c, g);
 #pragma unroll
-                        for (int pc = 0; pc < half / 64; ++pc) {
-                            if (lane == 0) bulk_wait_read0();      // the previous piece has left shared memory
-                            __syncwarp();
+                        for (int i = 0; i < 32; ++i) {
+                            const float pv = ex2(fmaf(g[i], kLog2e, -lse2));
+                            g[i] = c + i < nvr ? wt * (tl == c + i ? pv - 1.f : pv) : 0.f;
+                        }
 #pragma unroll
-                            for (int hh = 0; hh < 2; ++hh) {
-                                const int c = pc * 64 + hh * 32;
-                                float g[32];
-                                chunk(c, g);
+                        for (int part = 0; part < PARTS; ++part) {
+                            uint32_t u[16];
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) {
-                                    const float pv = ex2(fmaf(g[i], kLog2e, -lse2));
-                                    g[i] = c + i < nvr ? wt * (tl == c + i ? pv - 1.f : pv) : 0.f;
-                                    if (PARTS > 1) g[i] = bf16_part(g[i], part);
+                            for (int i = 0; i < 16; ++i) {
+                                u[i] = pack2(g[2 * i], g[2 * i + 1]);
+                                if (part + 1 < PARTS) {
+                                    g[2 * i] -= __uint_as_float(u[i] << 16);
+                                    g[2 * i + 1] -= __uint_as_float(u[i] & 0xffff0000u);
                                 }
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    st_shared_v4(piece + lane * 128 + (((hh * 4 + q) ^ (lane & 7)) << 4),
-                                                 pack2(g[8 * q], g[8 * q + 1]), pack2(g[8 * q + 2], g[8 * q + 3]),
-                                                 pack2(g[8 * q + 4], g[8 * q + 5]), pack2(g[8 * q + 6], g[8 * q + 7]));
                             }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0 && some) {
-                                tma_store_3d(&tm_a2, piece, (int)col0 + 64 * pc, (int)(T.mt * BM + HM * rank) + 32 * qd,
-                                             part);
-                                bulk_commit();
+                            if (some) {
+                                st_global_32(out + part * p.g_part + c, u);
+                                st_global_32(out + part * p.g_part + c + 16, u + 8);
                             }
                         }
                     }
@@ -628,7 +627,6 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                 ++tc;
             }
         }
-        if (lane == 0) bulk_wait0();
     }
 
     __syncwarp();
@@ -1161,10 +1159,9 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         const int64_t pw = a.v - v0 < L.piece ? a.v - v0 : L.piece;
         WPiece w;
         MOM_TRY(w_piece(a, L, v0, pw, w, true, st));
-        CUtensorMap mw_k, mw_mn, mg_st, mg_k, mg_mn;
+        CUtensorMap mw_k, mw_mn, mg_k, mg_mn;
         MOM_MAP(make_tma_3d(&mw_k, w.base, false, a.d, w.rows, PARTS, w.pitch, L.bn_logits / 2));
         MOM_MAP(make_tma_3d(&mw_mn, w.base, false, a.d, w.rows, PARTS, w.pitch, BK));
-        MOM_MAP(make_tma_3d(&mg_st, ws + L.g, false, L.piece, L.xrows, PARTS, L.piece, 32));
         MOM_MAP(make_tma_3d(&mg_k, ws + L.g, false, L.piece, L.xrows, PARTS, L.piece, HM));
         MOM_MAP(make_tma_3d(&mg_mn, ws + L.g, false, L.piece, L.xrows, PARTS, L.piece, BK));
         GemmArgs p{};
@@ -1176,10 +1173,13 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         p.targets = i32(L.targets);
         p.v0 = v0;
         p.vocab = a.v;
+        p.g = reinterpret_cast<bf16*>(ws + L.g);
+        p.g_pitch = L.piece;
+        p.g_part = L.xrows * L.piece;
         p.lse2 = f32(L.lse2);
         p.weight = a.dloss ? f32(L.weight) : nullptr;
         p.ws = a.ws;
-        MOM_TRY((run_gemm<PARTS, EPI_GRAD>(L.bn_logits, mx_k, mw_k, mg_st, mw_k, p, mt * cdiv(pw, L.bn_logits), true, st)));
+        MOM_TRY((run_gemm<PARTS, EPI_GRAD>(L.bn_logits, mx_k, mw_k, mx_k, mw_k, p, mt * cdiv(pw, L.bn_logits), true, st)));
         p.d = a.d;
         p.vec = vec;
         p.dx.rows = a.n;

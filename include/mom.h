@@ -846,8 +846,10 @@ mom_status mom_residual_norm_bwd(const void* x, const int8_t* x_codes, const flo
  *             target (both 0 when no row has one); mean may be NULL
  * loss, lse [n_rows] float32.  A target >= vocab is recorded in ws
  * (MOM_DEVERR_TARGET) and counts as padding.  x and w are 16-byte aligned; d
- * and vocab may be any sizes.  Products are on the bf16 tensor cores with
- * float32 accumulation; float32 operands are split into three bf16 parts.
+ * and vocab may be any sizes (n_rows and vocab up to 2^30, d up to 2^20, and
+ * at most 2^26 tiles of 256 x 128 in dx or dw: MOM_ERR_UNSUPPORTED).  Products
+ * are on the bf16 tensor cores with float32 accumulation; float32 operands are
+ * split into three bf16 parts.
  * ws: mom_linear_ce_workspace_size(.., backward = 0). */
 size_t mom_linear_ce_workspace_size(int64_t n_rows, int d, int64_t vocab, mom_dtype dt, int backward);
 mom_status mom_linear_ce_fwd(const void* x, const void* w, const int32_t* targets, mom_dtype dt, int64_t n_rows,
@@ -859,9 +861,11 @@ mom_status mom_linear_ce_fwd(const void* x, const void* w, const int32_t* target
  * NULL, of the mean loss), from the forward's lse: with g[t, v] = r[t] (exp(z
  * - lse) - [v = target]), 0 for padding rows,
  *   dx = g w [n_rows, d],  dw = g^T x [vocab, d]   (dt, overwritten)
- * The logits are formed again in pieces of the vocabulary and g is held for
- * one piece at a time (rounded to bf16, three bf16 parts for float32).  dx,
- * dw 16-byte aligned.  n_rows = 0 gives dw = 0.
+ * Padding rows take no part: their x and dloss may hold anything, and they
+ * cost nothing but the zeros of their dx.  The logits are formed again in
+ * pieces of the vocabulary and g, without dscale, is held for one piece at a
+ * time (rounded to bf16, three bf16 parts for float32); dscale multiplies the
+ * float32 sums.  dx, dw 16-byte aligned.  n_rows = 0 gives dw = 0.
  * ws: mom_linear_ce_workspace_size(.., backward = 1). */
 mom_status mom_linear_ce_bwd(const void* x, const void* w, const int32_t* targets, const float* lse,
                              const float* dloss, const float* dscale, mom_dtype dt, int64_t n_rows, int d,

@@ -1066,6 +1066,8 @@ static mom_status linear_ce_ok(const void* x, const void* w, const int32_t* targ
                                int64_t vocab, const void* ws, size_t ws_bytes, bool bwd) {
     if (!dt_ok(dt) || n_rows < 0 || d < 1 || vocab < 1) return MOM_ERR_ARG;
     if (n_rows > (1LL << 30) || vocab > (1LL << 30) || d > (1 << 20)) return MOM_ERR_UNSUPPORTED;
+    // the tiles of an output are counted in 32 bits
+    if (cdiv(n_rows > vocab ? n_rows : vocab, 256) * cdiv(d, 128) > (1LL << 26)) return MOM_ERR_UNSUPPORTED;
     if (!ws || !al16(ws) || ws_bytes < mom_linear_ce_workspace_size(n_rows, d, vocab, dt, bwd)) return MOM_ERR_ARG;
     if (n_rows > 0 && (!x || !w || !targets || !al16(x) || !al16(w) || !al(targets, 4))) return MOM_ERR_ARG;
     return MOM_OK;

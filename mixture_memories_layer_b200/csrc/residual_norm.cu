@@ -159,7 +159,7 @@ __device__ __forceinline__ void ask_l2(const void* p) { asm volatile("prefetch.g
 // HAS_Y: whether there is a block's output (the adjoint asks at run time)
 template <typename XT, typename T, typename G, bool VEC, int C, bool HAS_Y, bool BWD, int SRC> struct Rows {
     static_assert(C == 1 || SRC == DIRECT, "more than one chunk a warp: no registers to hold a row");
-    static constexpr int SLOTS = HAS_Y ? 3 : 5;
+    enum { SLOTS = HAS_Y ? 3 : 5 };
     typedef RawX<XT, VEC> X;
     typedef Raw8<T, VEC> Y;
     typedef Raw8<G, VEC> D;
@@ -397,6 +397,7 @@ template <typename XT, typename T, typename G, bool VEC, int C, int SRC, int MAX
 __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : 2)
 residual_norm_bwd_kernel(const ResNormArgs a, const ResNormBwdArgs b) {
     __shared__ __align__(16) float red[2][4][kMaxWarps];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int i = threadIdx.x; i < 8 * kMaxWarps; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     const int d = a.d;
@@ -574,6 +575,7 @@ __global__ void __launch_bounds__(1024) cols_reduce_kernel(const float* partial,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, which = blockIdx.y;
     float v = 0.f;
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // launched as the adjoint's CTAs leave
     if (c < d) {
         const float* at = partial + (int64_t)which * d + c;
 #pragma unroll 8
@@ -694,11 +696,20 @@ cudaError_t launch_residual_norm_bwd(const ResNormArgs& a, const ResNormBwdArgs&
         if (e != cudaSuccess) return e;
     }
     if (b.dw_post || b.dres_scale || b.dw_pre) {
-        cols_reduce_kernel<<<dim3((unsigned)cdiv(a.d, 32), 2), 1024, 0, st>>>(b.partial, parts, a.d, a.w_post, a.res_scale,
-                                                                    b.dw_post, b.dres_scale, b.dw_pre);
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)cdiv(a.d, 32), 2);
+        cfg.blockDim = dim3(1024);
+        cfg.stream = st;
+        cfg.attrs = &at;
+        cfg.numAttrs = parts > 0 ? 1 : 0;
         count_launches(1);
+        return cudaLaunchKernelEx(&cfg, cols_reduce_kernel, (const float*)b.partial, parts, a.d, a.w_post, a.res_scale,
+                                  b.dw_post, b.dres_scale, b.dw_pre);
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace mom

@@ -54,6 +54,10 @@ class MoMStack:
         return (self._buf("codes%d" % i, (n, self.d_model), torch.int8),
                 self._buf("scales%d" % i, (n, groups), torch.float32))
 
+    def _check_gates(self, gates):
+        if gates is not None and len(gates) != len(self.blocks):
+            raise ValueError("gates has %d entries for %d blocks" % (len(gates), len(self.blocks)))
+
     def _w_next(self, i):
         return self.norms[i + 1]["w_pre"] if i + 1 < len(self.blocks) else self.w_final
 
@@ -65,6 +69,7 @@ class MoMStack:
         [N, d_model] in the blocks' type).  Returns ``h`` [N, d_model], the
         normed output, and ``x``, the stream after the last block (both
         written again by the next call); x itself is left as it is."""
+        self._check_gates(gates)
         n = x.shape[0]
         st = stream if stream is not None else torch.cuda.current_stream()
         h = self._buf("h", (n, self.d_model), self.dtype)
@@ -87,6 +92,7 @@ class MoMStack:
         float32, the gradient of the input stream, ``dw_final`` and ``levels``:
         for each block dw_pre, dw_post, dres_scale, dgate (where it has them)
         and ``block``, the block's own gradients (MoMBlock.backward)."""
+        self._check_gates(gates)
         n = dh.shape[0]
         st = stream if stream is not None else torch.cuda.current_stream()
         f32 = torch.float32
@@ -129,6 +135,7 @@ class MoMStack:
         """One token a sequence: x [B, d_model] (stream_dtype); states: for
         each block (state, conv_sh, conv_mem) of MoMBlock.decode_step, updated
         in place.  Returns ``h`` and ``x`` as forward."""
+        self._check_gates(gates)
         n = x.shape[0]
         st = stream if stream is not None else torch.cuda.current_stream()
         h = self._buf("dec_h", (n, self.d_model), self.dtype)

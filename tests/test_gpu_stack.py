@@ -168,3 +168,6 @@ def test_a_stack_refuses_what_it_cannot_hold():
         MoMStack([b], [n, n], stack.w_final)
     with pytest.raises(ValueError):
         MoMStack([], [], stack.w_final)
+    with pytest.raises(ValueError, match="gates"):
+        stack.forward(torch.zeros((4, w.d_model), dtype=BF, device="cuda"),
+                      torch.tensor([0, 4], dtype=torch.int32, device="cuda"), gates=[None, None])

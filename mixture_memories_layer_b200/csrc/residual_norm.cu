@@ -11,10 +11,14 @@
 //   dgate = D s w_post n_y sigma (1 - sigma)        (its row's sum for one gate a token)
 //   A    = sum_t D sigma n_y,  dw_post = s A,  ds = w_post A,  dw_pre = sum_t dh n_x
 //
-// Bound by memory.  A row lives in the registers of W warps (C chunks of 256
-// channels each), every operand is read once and all of a row's loads are
-// issued before its first reduction.  Sums, norms and the whole arithmetic
-// are float32; each output is rounded once, as it is stored.
+// Bound by memory, and nearly as much by issuing instructions (65 % of the
+// issue slots with 16 warps an SM).  A row is spread over the W warps of a CTA,
+// C chunks of 256 channels a warp; every operand is read from memory once and
+// later rows' operands are on their way while one is worked on.  Sums, norms
+// and the whole arithmetic are float32; each output is rounded once, as it is
+// stored.  16384 x 1024 bf16 with an element gate: forward 35 us, 4.8 TB/s;
+// adjoint with float32 gradients and the stream from its checkpoint 73 us, 4.8
+// TB/s (a plain copy of 4 GB: 6.6).
 #include <type_traits>
 
 #include "rows8.cuh"
@@ -131,15 +135,18 @@ template <bool VEC, int C> struct Weights {
     }
 };
 
-// Where the rows' operands come from.  With one chunk a warp a row's operands
-// are held in registers, packed, while it is worked on:
-//   RING    copies in flight to slots in shared memory, two rows ahead (four
-//           without a block's output, when a row is short); each thread reads
-//           only what it copied itself (no barrier), and a slot is filled again
-//           one row after it was read
-//   REGS    loads into registers one row ahead
+// Where the rows' operands come from.
+//   RING    the forward's rows of up to 8192 channels that 16-byte copies take:
+//           copies in flight to slots in shared memory, the slots but one rows
+//           ahead (more without a block's output, when a row is short); each
+//           thread reads only what it copied itself (no barrier), into
+//           registers, and a slot is filled again one row after it was read
+//   REGS    loads into registers one row ahead, one chunk a warp
 //   DIRECT  loads when the row's turn comes, its lines asked into L2 one row
-//           ahead.  Wider rows are read at each use, the later ones from L1.
+//           ahead: the adjoint's rows that 16-byte loads cannot take, and wide
+//           rows, which are read again at each use, from L1
+// 16 M elements bf16, d 8192, forward: 49 us by RING, 64 us by DIRECT; 3001 x
+// 1021 float32, adjoint: 23 us by DIRECT, 31 us by REGS, which spill.
 enum Source { RING, REGS, DIRECT };
 
 template <typename R> __device__ __forceinline__ void take_f2(const R& r, f2 (&v)[4]) {
@@ -158,8 +165,9 @@ __device__ __forceinline__ void ask_l2(const void* p) { asm volatile("prefetch.g
 
 // HAS_Y: whether there is a block's output (the adjoint asks at run time)
 template <typename XT, typename T, typename G, bool VEC, int C, bool HAS_Y, bool BWD, int SRC> struct Rows {
-    static_assert(C == 1 || SRC == DIRECT, "more than one chunk a warp: no registers to hold a row");
-    enum { SLOTS = HAS_Y ? 3 : 5 };
+    static constexpr bool HOLD = C == 1 || SRC == RING;      // the registers hold a row
+    static_assert(SRC != REGS || C == 1, "");
+    enum { SLOTS = C == 2 ? (HAS_Y ? 2 : 4) : HAS_Y ? 3 : 5 };
     typedef RawX<XT, VEC> X;
     typedef Raw8<T, VEC> Y;
     typedef Raw8<G, VEC> D;
@@ -172,7 +180,7 @@ template <typename XT, typename T, typename G, bool VEC, int C, bool HAS_Y, bool
     const ResNormBwdArgs& b;
     int W, warp, lane;
     int64_t row, step;
-    Held cur, next;                          // one chunk a warp; REGS: the next row's
+    Held cur[HOLD ? C : 1], next;            // REGS: the next row's
     uint32_t base, pitch, bytes;             // RING
     int in, out;
 
@@ -193,30 +201,38 @@ template <typename XT, typename T, typename G, bool VEC, int C, bool HAS_Y, bool
         if constexpr (SRC == RING) {
             pitch = blockDim.x * 16;
             base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
-            bytes = pieces(a) * pitch;
+            bytes = C * pieces(a) * pitch;
             in = out = 0;
 #pragma unroll
             for (int i = 0; i < SLOTS - 1; ++i) put(row + i * step);
         } else if constexpr (SRC == REGS) {
-            load(next, first);
+            load(next, first, 0);
         }
     }
-    __device__ __forceinline__ void load(Held& o, int64_t r) {
+    __device__ __forceinline__ void load(Held& o, int64_t r, int j) {
         if (r >= a.n_rows) return;
-        if (has_y()) o.y.load(at_y(r), c0(0), a.d, lane);
-        o.x.load(a, r, c0(0), lane);
-        if (elem()) o.g.load(at_g(r), c0(0), a.d, lane);
-        if (BWD && b.dh) o.h.load(at_h(r), c0(0), a.d, lane);
-        if (BWD && b.dx_out) o.d.load(at_d(r), c0(0), a.d, lane);
+        if (has_y()) o.y.load(at_y(r), c0(j), a.d, lane);
+        o.x.load(a, r, c0(j), lane);
+        if (elem()) o.g.load(at_g(r), c0(j), a.d, lane);
+        if (BWD && b.dh) o.h.load(at_h(r), c0(j), a.d, lane);
+        if (BWD && b.dx_out) o.d.load(at_d(r), c0(j), a.d, lane);
     }
     __device__ __forceinline__ void put(int64_t r) {
         if (r < a.n_rows) {
             uint32_t at = base + in * bytes;
-            X::copy(at, pitch, a, r, c0(0), lane);
-            at += X::PIECES * pitch;
-            if (HAS_Y) Y::copy(at, pitch, at_y(r), c0(0), a.d, lane);
-            at += Y::PIECES * pitch;
-            if (elem()) Y::copy(at, pitch, at_g(r), c0(0), a.d, lane);
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                X::copy(at, pitch, a, r, c0(j), lane);
+                at += X::PIECES * pitch;
+                if (HAS_Y) {
+                    Y::copy(at, pitch, at_y(r), c0(j), a.d, lane);
+                    at += Y::PIECES * pitch;
+                }
+                if (elem()) {
+                    Y::copy(at, pitch, at_g(r), c0(j), a.d, lane);
+                    at += Y::PIECES * pitch;
+                }
+            }
         }
         in = in + 1 == SLOTS ? 0 : in + 1;
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -224,11 +240,19 @@ template <typename XT, typename T, typename G, bool VEC, int C, bool HAS_Y, bool
     __device__ __forceinline__ void take() {
         asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 2) : "memory");      // all but the youngest
         uint32_t at = base + out * bytes;
-        cur.x.take(at, pitch);
-        at += X::PIECES * pitch;
-        if (HAS_Y) cur.y.take(at, pitch);
-        at += Y::PIECES * pitch;
-        if (elem()) cur.g.take(at, pitch);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            cur[j].x.take(at, pitch);
+            at += X::PIECES * pitch;
+            if (HAS_Y) {
+                cur[j].y.take(at, pitch);
+                at += Y::PIECES * pitch;
+            }
+            if (elem()) {
+                cur[j].g.take(at, pitch);
+                at += Y::PIECES * pitch;
+            }
+        }
         out = out + 1 == SLOTS ? 0 : out + 1;
     }
     __device__ __forceinline__ void ask(int64_t r) const {
@@ -251,37 +275,40 @@ template <typename XT, typename T, typename G, bool VEC, int C, bool HAS_Y, bool
             take();
             put(row + (SLOTS - 1) * step);
         } else if constexpr (SRC == REGS) {
-            cur = next;
-            load(next, row + step);
+            cur[0] = next;
+            load(next, row + step, 0);
         } else {
-            if constexpr (C == 1) load(cur, row);
+            if constexpr (HOLD) {
+#pragma unroll
+                for (int j = 0; j < C; ++j) load(cur[j], row, j);
+            }
             ask(row + step);
         }
     }
     __device__ __forceinline__ void x(int j, X& o) const {
-        if constexpr (C == 1) o = cur.x;
+        if constexpr (HOLD) o = cur[j].x;
         else o.load(a, row, c0(j), lane);
     }
     __device__ __forceinline__ void y(int j, f2 (&v)[4]) const {
-        if constexpr (C == 1) { take_f2(cur.y, v); return; }
+        if constexpr (HOLD) { take_f2(cur[j].y, v); return; }
         Y o;
         o.load(at_y(row), c0(j), a.d, lane);
         take_f2(o, v);
     }
     __device__ __forceinline__ void g(int j, f2 (&v)[4]) const {
-        if constexpr (C == 1) { take_f2(cur.g, v); return; }
+        if constexpr (HOLD) { take_f2(cur[j].g, v); return; }
         Y o;
         o.load(at_g(row), c0(j), a.d, lane);
         take_f2(o, v);
     }
     __device__ __forceinline__ void h(int j, f2 (&v)[4]) const {
-        if constexpr (C == 1) { take_f2(cur.h, v); return; }
+        if constexpr (HOLD) { take_f2(cur[j].h, v); return; }
         D o;
         o.load(at_h(row), c0(j), a.d, lane);
         take_f2(o, v);
     }
     __device__ __forceinline__ void d(int j, f2 (&v)[4]) const {
-        if constexpr (C == 1) { take_f2(cur.d, v); return; }
+        if constexpr (HOLD) { take_f2(cur[j].d, v); return; }
         D o;
         o.load(at_d(row), c0(j), a.d, lane);
         take_f2(o, v);
@@ -619,7 +646,7 @@ constexpr int kSmemSM = 220 * 1024;
 
 template <typename XT, typename T, bool VEC, int C, bool HAS_Y, int MAXT>
 cudaError_t run_fwd(ResNormArgs a, cudaStream_t st) {
-    constexpr int SRC = C > 1 ? DIRECT : VEC ? RING : REGS;
+    constexpr int SRC = C <= 2 && VEC ? RING : C == 1 ? REGS : DIRECT;
     auto* kernel = residual_norm_kernel<XT, T, VEC, C, HAS_Y, SRC, MAXT>;
     const int W = shape_for(a.d).warps, threads = W == 1 ? 128 : 32 * W;
     a.warps_per_row = W;
@@ -627,8 +654,8 @@ cudaError_t run_fwd(ResNormArgs a, cudaStream_t st) {
     size_t smem = 0;
     if (SRC == RING) {
         typedef Rows<XT, T, T, VEC, C, HAS_Y, false, SRC> R;
-        // at most 16 warps x 6 pieces x 3 slots, or 32 x 2 x 5: 160 KB an SM
-        smem = (size_t)R::SLOTS * R::pieces(a) * threads * 16;
+        // at most 16 warps x 12 pieces x 2 slots, or 32 x 2 x 5: 192 KB an SM
+        smem = (size_t)R::SLOTS * R::pieces(a) * C * threads * 16;
         static unsigned long long optin_done = 0;
         const cudaError_t e = smem_optin((const void*)kernel, kSmemSM, &optin_done);
         if (e != cudaSuccess) return e;

@@ -965,7 +965,7 @@ Plan plan_for(int64_t n, int d, int64_t v, int dt, bool bwd) {
     if (piece < 256) piece = 256;
     const int64_t np = cdiv(v, piece);
     L.piece = up(cdiv(v, np), 256);
-    size_t o = MOM_WS_HEADER_BYTES;
+    size_t o = MOM_WS_HEADER_BYTES;      // from the workspace's first 256-byte boundary on (ws_base)
     auto take = [&](size_t b) { const size_t at = o; o += up256(b); return at; };
     if (!L.direct) L.wbuf = take((size_t)L.parts * L.piece * L.pitch * 2);
     if (!L.direct || bwd) L.xbuf = take((size_t)L.parts * L.xrows * L.pitch * 2);
@@ -1002,7 +1002,7 @@ Plan plan_for(int64_t n, int d, int64_t v, int dt, bool bwd) {
         L.live = take(4);
         L.counts = take(cdiv(n, kCountRows) * 4);
     }
-    L.bytes = o;
+    L.bytes = o + 240;
     return L;
 }
 
@@ -1057,6 +1057,9 @@ int64_t join_grid(int64_t rows, int d) {
     return b < most ? b : most;
 }
 
+// A workspace is 16-byte aligned; its arrays start at multiples of 256 (g's rows take 32-byte stores).
+inline char* ws_base(void* ws) { return reinterpret_cast<char*>(up(static_cast<int64_t>(reinterpret_cast<uintptr_t>(ws)), 256)); }
+
 // the piece of W from class v0 on as a TMA operand: in place, or copied
 struct WPiece {
     const void* base;
@@ -1068,7 +1071,7 @@ cudaError_t w_piece(const LinearCeArgs& a, const Plan& L, int64_t v0, int64_t pw
         w = WPiece{a.w, (uint64_t)a.v, (uint64_t)a.d, (int)v0};
         return cudaSuccess;
     }
-    char* buf = reinterpret_cast<char*>(a.ws) + L.wbuf;
+    char* buf = ws_base(a.ws) + L.wbuf;
     w = WPiece{buf, (uint64_t)pw, (uint64_t)L.pitch, 0};
     const size_t es = a.dt == MOM_BF16 ? 2 : 4;
     return to_parts(reinterpret_cast<const char*>(a.w) + (size_t)v0 * a.d * es, a.dt, pw, a.d, L.pitch, buf, next, st);
@@ -1079,7 +1082,7 @@ cudaError_t w_piece(const LinearCeArgs& a, const Plan& L, int64_t v0, int64_t pw
 
 template <int PARTS> cudaError_t fwd(const LinearCeArgs& a, cudaStream_t st) {
     const Plan L = plan_for(a.n, a.d, a.v, a.dt, false);
-    char* ws = reinterpret_cast<char*>(a.ws);
+    char* ws = ws_base(a.ws);
     if (!L.direct) MOM_TRY(to_parts(a.x, a.dt, a.n, a.d, L.pitch, ws + L.xbuf, false, st));
     const void* xb = L.direct ? a.x : ws + L.xbuf;
     int n_part = 0;
@@ -1123,7 +1126,7 @@ template <int PARTS> cudaError_t fwd(const LinearCeArgs& a, cudaStream_t st) {
 template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
     typedef typename std::conditional<PARTS == 1, bf16, float>::type T;
     const Plan L = plan_for(a.n, a.d, a.v, a.dt, true);
-    char* ws = reinterpret_cast<char*>(a.ws);
+    char* ws = ws_base(a.ws);
     auto i32 = [&](size_t at) { return reinterpret_cast<int32_t*>(ws + at); };
     auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
     const bool vec = a.d % (16 / (int)sizeof(T)) == 0;         // of dx's and dw's rows

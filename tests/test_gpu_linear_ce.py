@@ -361,3 +361,20 @@ def test_gradients_are_differences_of_the_loss():
                 out.append(loss.sum() / (tg >= 0).sum())
             got, want = float((out[0] - out[1]) / (2 * e)), float((grads[name] * a).sum())
             assert abs(got - want) < 2.0 ** -11 + 2.0 ** -13, (name, got, want)
+
+
+@pytest.mark.parametrize("t,d", [("bf16", 72), ("f32", 65)])
+def test_a_workspace_at_any_16_bytes(t, d):
+    from mixture_memories_layer_b200 import binding as B
+    n, v = 130, 700
+    x, w, tg = _problem(n, d, v, t, seed=25)
+    outs = []
+    for off in (0, 16, 48, 240):
+        loss, lse, mean = (torch.empty(k, device="cuda") for k in (n, n, 2))
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        ws = [B.new_workspace(B.mom_linear_ce_workspace_size(n, d, v, DT[t], b) + off)[off:] for b in (0, 1)]
+        B.mom_linear_ce_fwd(x, w, tg, loss, lse, mean, ws[0])
+        B.mom_linear_ce_bwd(x, w, tg, lse, None, mean[1:2], dx, dw, ws[1])
+        assert all(B.mom_get_error(a) == (0, 0) for a in ws)
+        outs.append((loss, lse, mean, dx, dw))
+    assert all(torch.equal(a, b) for o in outs[1:] for a, b in zip(o, outs[0]))

@@ -978,8 +978,11 @@ Plan plan_for(int64_t n, int d, int64_t v, int dt, bool bwd) {
         L.sums = take((size_t)cdiv(n, 32) * 8);
         L.ticket = take(4);
     } else {
-        // 128 columns where 256 would leave a quarter or more of them empty
-        L.bn = d <= 128 || (d > 256 && d <= 384) ? 128 : 256;
+        // 128 columns where 256 would leave a quarter or more of them empty;
+        // float32, whose six products need fewer bytes each, a tenth (1001 x
+        // 515 x 8009: 248 us, 254 us with 256)
+        const int64_t narrow = up(d, 128), wide = up(d, 256);
+        L.bn = (b16 ? narrow * 4 <= wide * 3 : narrow * 11 < wide * 10) ? 128 : 256;
         L.bn_logits = columns_for(n, L.piece < v ? L.piece : v, d, L.parts, clusters);
         // K blocks of a tile, and of a cluster's share of a piece, each tile's
         // epilogue counted as 4 of them (float32, six products a block: as 1)

@@ -589,12 +589,12 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                     }
                 } else {
                     // g is 0 past the vocabulary and past the packed rows, up to whole
-                    // K blocks of dW.  A lane writes its row in 32-byte sectors, past
+                    // K blocks of dW (or n, past which TMA fills in zeros).  A lane writes its row in 32-byte sectors, past
                     // shared memory: the MMAs' operands and the copies that bring them
                     // take all of its bandwidth.
                     const int nvr = row < live ? nv : 0;
                     bf16* out = p.g + row * p.g_pitch + col0;
-                    const bool some = row < cdiv(live, BK) * BK;
+                    const bool some = row < cdiv(live, BK) * BK && row < p.rows;
 #pragma unroll
                     for (int c = 0; c < half; c += 32) {
                         float g[32];
@@ -647,40 +647,43 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
 }
 
 // ------------------------------------------------------------ small kernels
-// The sum of a product's slots, in order, as its rows of the output: a block
-// for 32 rows x 32 columns, 8 columns a warp, four slots in flight.
+// The sum of a product's slots as its rows of the output: a block for 32 rows
+// x 32 columns.  A warp sums 8 columns of every fourth slot, in order and four
+// at a time; the four sums are added in order.
 template <typename T>
-__global__ void __launch_bounds__(128) join_kernel(const Prod q, const int32_t* live, int d) {
-    __shared__ float tile[32][33];
+__global__ void __launch_bounds__(512) join_kernel(const Prod q, const int32_t* live, int d) {
+    __shared__ float tile[4][32][33];
     after_previous();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cw = warp & 3, sg = warp >> 2;
     const int64_t rows = live ? *live : q.rows, cb = cdiv(d, 32), total = cdiv(rows, 32) * cb;
     const float f = q.scale ? *q.scale : 1.f;
     for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
         const int64_t rb = u / cb, col = (u - rb * cb) * 32;
         const int64_t stride = partial_at(q, d, 1, 0, 0) - q.partial;
-        const float* at = partial_at(q, d, 0, rb, col + 8 * warp) + lane;
+        const float* at = partial_at(q, d, 0, rb, col + 8 * cw) + lane;
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < q.slots; s += 4) {
+        for (int s = sg; s < q.slots; s += 16) {
             float w[4][8];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[k][i] = s + k < q.slots ? at[(s + k) * stride + i * 32] : 0.f;
+                for (int i = 0; i < 8; ++i) w[k][i] = s + 4 * k < q.slots ? at[(s + 4 * k) * stride + i * 32] : 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] += w[k][i];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) tile[lane][8 * warp + i] = v[i] * f;
+        for (int i = 0; i < 8; ++i) tile[sg][lane][8 * cw + i] = v[i];
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t row = rb * 32 + 8 * warp + i;
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * warp + i;
+            const int64_t row = rb * 32 + r;
             if (row < rows && col + lane < d) {
                 const int64_t to = q.row_of ? q.row_of[row] : q.row0 + row;
-                reinterpret_cast<T*>(q.out)[to * d + col + lane] = from_f<T>(tile[8 * warp + i][lane]);
+                const float sum = (tile[0][r][lane] + tile[1][r][lane]) + (tile[2][r][lane] + tile[3][r][lane]);
+                reinterpret_cast<T*>(q.out)[to * d + col + lane] = from_f<T>(sum * f);
             }
         }
         __syncthreads();
@@ -908,10 +911,10 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
         }
     }
     if (r0 + kGatherRows < a.n) return;
-    // the last block: the number of rows, and zeros up to whole K blocks of dW
+    // the last block: the number of rows, and zeros up to whole K blocks of dW (or n)
     const int64_t live = before + __popc(in);
     if (threadIdx.x == 0) *a.live = (int32_t)live;
-    for (int64_t r = live + warp; r < cdiv(live, BK) * BK; r += 8)
+    for (int64_t r = live + warp; r < cdiv(live, BK) * BK && r < a.n; r += 8)
         for (int q = 0; q < PARTS; ++q)
             for (int c = lane * 2; c < a.d; c += 64)
                 *reinterpret_cast<__nv_bfloat162*>(a.xc + q * a.part + r * a.pitch + c) = __floats2bfloat162_rn(0.f, 0.f);
@@ -936,7 +939,6 @@ struct Plan {
     bool direct;           // x (forward) and w are read in place by TMA
     int pitch;             // row pitch of copied operands (elements)
     int64_t piece;         // classes of a piece (a multiple of 256)
-    int64_t xrows;         // rows of the packed x
     int bn, bn_logits;     // columns of a tile: OUT; STATS or GRAD
     int sx, sw;            // K slots of dx and dw
     bool dx_partial, dw_partial;
@@ -960,7 +962,6 @@ Plan plan_for(int64_t n, int d, int64_t v, int dt, bool bwd) {
     L.parts = b16 ? 1 : 3;
     L.direct = b16 && d % 8 == 0;
     L.pitch = (int)up(d, 8);
-    L.xrows = bwd ? up(n, BK) : n;
     int64_t piece = kPieceBytes / (2 * L.parts * (n > L.pitch ? n : L.pitch)) / 256 * 256;
     if (piece < 256) piece = 256;
     const int64_t np = cdiv(v, piece);
@@ -968,7 +969,7 @@ Plan plan_for(int64_t n, int d, int64_t v, int dt, bool bwd) {
     size_t o = MOM_WS_HEADER_BYTES;      // from the workspace's first 256-byte boundary on (ws_base)
     auto take = [&](size_t b) { const size_t at = o; o += up256(b); return at; };
     if (!L.direct) L.wbuf = take((size_t)L.parts * L.piece * L.pitch * 2);
-    if (!L.direct || bwd) L.xbuf = take((size_t)L.parts * L.xrows * L.pitch * 2);
+    if (!L.direct || bwd) L.xbuf = take((size_t)L.parts * n * L.pitch * 2);
     if (!bwd) {
         const int64_t rows = n < kRowChunk ? n : kRowChunk;
         L.zt = take(rows * 4);
@@ -995,7 +996,7 @@ Plan plan_for(int64_t n, int d, int64_t v, int dt, bool bwd) {
         L.sw = (int)cdiv(k2, share);
         L.dx_partial = L.sx > 1 || L.piece < v;
         L.dw_partial = L.sw > 1;
-        L.g = take((size_t)L.parts * L.xrows * L.piece * 2);
+        L.g = take((size_t)L.parts * n * L.piece * 2);
         if (L.dx_partial) L.dxp = take((size_t)L.sx * up(n, 32) * up(d, 32) * 4);
         if (L.dw_partial) L.dwp = take((size_t)L.sw * up(L.piece, 32) * up(d, 32) * 4);
         L.targets = take(n * 4);
@@ -1056,7 +1057,7 @@ cudaError_t to_parts(const void* src, int dt, int64_t rows, int d, int pitch, vo
 }
 
 int64_t join_grid(int64_t rows, int d) {
-    const int64_t b = cdiv(rows, 32) * cdiv(d, 32), most = (int64_t)sm_count() * 16;
+    const int64_t b = cdiv(rows, 32) * cdiv(d, 32), most = (int64_t)sm_count() * 4;
     return b < most ? b : most;
 }
 
@@ -1146,7 +1147,7 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         g.vocab = a.v;
         g.d = a.d;
         g.pitch = L.pitch;
-        g.part = L.xrows * L.pitch;
+        g.part = a.n * L.pitch;
         g.xc = xc;
         g.targets_c = i32(L.targets);
         g.row_of = i32(L.row_of);
@@ -1161,8 +1162,8 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         MOM_TRY(launch(gather_kernel<T, PARTS>, cdiv(a.n, kGatherRows), 256, 0, a.n > kCountRows, st, g));
     }
     CUtensorMap mx_k, mx_mn;       // x: K-major rows of the logits; MN-major rows (K = tokens) of dw
-    MOM_MAP(make_tma_3d(&mx_k, xc, false, a.d, L.xrows, PARTS, L.pitch, HM));
-    MOM_MAP(make_tma_3d(&mx_mn, xc, false, a.d, L.xrows, PARTS, L.pitch, BK));
+    MOM_MAP(make_tma_3d(&mx_k, xc, false, a.d, a.n, PARTS, L.pitch, HM));
+    MOM_MAP(make_tma_3d(&mx_mn, xc, false, a.d, a.n, PARTS, L.pitch, BK));
     const int64_t mt = cdiv(a.n, BM);
     for (int64_t v0 = 0; v0 < a.v; v0 += L.piece) {
         const int64_t pw = a.v - v0 < L.piece ? a.v - v0 : L.piece;
@@ -1171,8 +1172,8 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         CUtensorMap mw_k, mw_mn, mg_k, mg_mn;
         MOM_MAP(make_tma_3d(&mw_k, w.base, false, a.d, w.rows, PARTS, w.pitch, L.bn_logits / 2));
         MOM_MAP(make_tma_3d(&mw_mn, w.base, false, a.d, w.rows, PARTS, w.pitch, BK));
-        MOM_MAP(make_tma_3d(&mg_k, ws + L.g, false, L.piece, L.xrows, PARTS, L.piece, HM));
-        MOM_MAP(make_tma_3d(&mg_mn, ws + L.g, false, L.piece, L.xrows, PARTS, L.piece, BK));
+        MOM_MAP(make_tma_3d(&mg_k, ws + L.g, false, L.piece, a.n, PARTS, L.piece, HM));
+        MOM_MAP(make_tma_3d(&mg_mn, ws + L.g, false, L.piece, a.n, PARTS, L.piece, BK));
         GemmArgs p{};
         p.rows = a.n;
         p.cols = pw;
@@ -1184,7 +1185,7 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         p.vocab = a.v;
         p.g = reinterpret_cast<bf16*>(ws + L.g);
         p.g_pitch = L.piece;
-        p.g_part = L.xrows * L.piece;
+        p.g_part = a.n * L.piece;
         p.lse2 = f32(L.lse2);
         p.weight = a.dloss ? f32(L.weight) : nullptr;
         p.ws = a.ws;
@@ -1211,8 +1212,8 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         const int64_t nt = cdiv(a.d, L.bn), tiles = mt * nt * L.sx + cdiv(pw, BM) * nt * L.sw;
         MOM_TRY((run_gemm<PARTS, EPI_OUT>(L.bn, mg_k, mw_mn, mg_mn, mx_mn, p, tiles, true, st)));
         if (L.sx > 1 && p.dx.last)
-            MOM_TRY(launch(join_kernel<T>, join_grid(a.n, a.d), 128, 0, true, st, p.dx, live, a.d));
-        if (L.sw > 1) MOM_TRY(launch(join_kernel<T>, join_grid(pw, a.d), 128, 0, true, st, p.dw, (const int32_t*)nullptr, a.d));
+            MOM_TRY(launch(join_kernel<T>, join_grid(a.n, a.d), 512, 0, true, st, p.dx, live, a.d));
+        if (L.sw > 1) MOM_TRY(launch(join_kernel<T>, join_grid(pw, a.d), 512, 0, true, st, p.dw, (const int32_t*)nullptr, a.d));
     }
     return cudaSuccess;
 }

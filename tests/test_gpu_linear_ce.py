@@ -309,10 +309,12 @@ def test_padding_rows_may_hold_anything(t, d):
 
 @pytest.mark.parametrize("n,d,v,t,pad", [(20000, 64, 700, "bf16", 0.8), (40000, 40, 300, "f32", 0.5), (16385, 72, 257, "bf16", 0.1),
                                          (12000, 512, 1000, "bf16", 0.0), (4096, 64, 132000, "bf16", 0.3),
-                                         (200, 360, 8000, "f32", 0.1), (3000, 300, 6000, "f32", 0.1)])
+                                         (200, 360, 8000, "f32", 0.1), (3000, 300, 6000, "f32", 0.1),
+                                         (70000, 33, 9000, "bf16", 0.3), (40000, 41, 5000, "f32", 0.3)])
 def test_long_batches_and_slots(n, d, v, t, pad):
     """Rows counted in chunks (n > 16384), token and vocabulary axes split into
-    slots, several pieces with slots, tiles of 128 and 256 columns; by 2-norm,
+    slots, several pieces with slots, several pieces of ragged rows, tiles of
+    128 and 256 columns; by 2-norm,
     bf16 two roundings of at most 2^-8 each, float32 1e-5 (a logit's float32
     error in its exponential is the largest)."""
     from mixture_memories_layer_b200.lm_head import LMHead

@@ -264,38 +264,48 @@ struct Schedule {
 };
 
 // ------------------------------------------------------------- outputs --
-// 32 columns of 32 rows (lane = row, v = its columns from `col` on) to the
-// rows `row` (< 0: none) of out [.., ld], 16 bytes a store and up to the last
-// 16 bytes that hold a column below d: through the warp's staging, so that a
-// store covers whole sectors.
-template <typename T>
-__device__ __forceinline__ void emit(T* out, int64_t ld, int d, int64_t row, int64_t col, const float* v, uint32_t piece,
-                                     int lane) {
-    constexpr int Q = 2 * sizeof(T);               // 16-byte chunks of a row
-    __syncwarp();
+// Tiles' rows go to memory through the warp's staging, 32 columns of 32 rows at
+// a time, so that a store covers whole sectors: a row is 2 sizeof(T) chunks of
+// 16 bytes, and lane l moves chunk l % Q of rows l / Q, + 32 / Q, ..
+template <typename T> struct Emit {
+    static constexpr int Q = 2 * sizeof(T), E = 16 / sizeof(T), RI = 32 / Q;
+    int32_t to[Q];                                 // output rows of the lane's chunks (< 0: none)
+    __device__ __forceinline__ void rows(int32_t row, int lane) {      // row: lane's row of the tile
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        const uint32_t at = piece + lane * (16 * Q) + ((sizeof(T) == 4 ? q ^ (lane & 7) : q ^ ((lane >> 1) & 3)) << 4);
-        if constexpr (sizeof(T) == 4)
-            st_shared_v4(at, __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
-                         __float_as_uint(v[4 * q + 3]));
-        else
-            st_shared_v4(at, pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
-                         pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7]));
+        for (int it = 0; it < Q; ++it) to[it] = __shfl_sync(0xffffffffu, row, it * RI + lane / Q);
     }
-    __syncwarp();
-    constexpr int E = 16 / sizeof(T), RI = 32 / Q;      // elements of a chunk, rows an iteration
-    const int q = lane % Q;
+    static __device__ __forceinline__ uint32_t at(uint32_t piece, int r, int q) {
+        return piece + r * (16 * Q) + ((sizeof(T) == 4 ? q ^ (r & 7) : q ^ ((r >> 1) & 3)) << 4);
+    }
+    // v: lane's row's columns from `col` on, into out [.., ld], up to the last
+    // 16 bytes that hold a column below d
+    __device__ __forceinline__ void put(T* out, int64_t ld, int d, int64_t col, const float* v, uint32_t piece,
+                                        int lane) const {
+        __syncwarp();
 #pragma unroll
-    for (int it = 0; it < Q; ++it) {
-        const int r = it * RI + lane / Q;
-        const int64_t to = __shfl_sync(0xffffffffu, row, r);
-        uint32_t a, b, c, e;
-        const uint32_t at = piece + r * (16 * Q) + ((sizeof(T) == 4 ? q ^ (r & 7) : q ^ ((r >> 1) & 3)) << 4);
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(e) : "r"(at) : "memory");
-        if (to >= 0 && col + q * E < d) *reinterpret_cast<uint4*>(out + to * ld + col + q * E) = make_uint4(a, b, c, e);
+        for (int q = 0; q < Q; ++q) {
+            if constexpr (sizeof(T) == 4)
+                st_shared_v4(at(piece, lane, q), __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                             __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+            else
+                st_shared_v4(at(piece, lane, q), pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
+                             pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7]));
+        }
+        __syncwarp();
+        const int q = lane % Q;
+        uint4 u[Q];
+#pragma unroll
+        for (int it = 0; it < Q; ++it)
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(u[it].x), "=r"(u[it].y), "=r"(u[it].z), "=r"(u[it].w)
+                         : "r"(at(piece, it * RI + lane / Q, q)));
+        if (col + q * E >= d) return;
+        T* o = out + col + q * E;
+#pragma unroll
+        for (int it = 0; it < Q; ++it)
+            if (to[it] >= 0) *reinterpret_cast<uint4*>(o + to[it] * ld) = u[it];
     }
-}
+};
 
 // A partial's element of row block rb, column col, lane 0.
 __device__ __forceinline__ float* partial_at(const Prod& q, int d, int slot, int64_t rb, int64_t col) {
@@ -440,6 +450,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
         const uint32_t piece = smem_u32(sOut + e * PIECE);
         const uint32_t lead_tempty = leader_addr(tempty0);
         const int64_t live = p.live ? *p.live : p.rows;
+        const float scale = EPI == EPI_OUT && p.dx.scale ? *p.dx.scale : 1.f;      // (of dw as well)
         uint32_t tc = 0;
         bool ok = true;
         for (uint32_t j = 0; S.at(EPI, j, T); ++j) {
@@ -504,11 +515,11 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                 const Prod& q = T.dw ? p.dw : p.dx;
                 const int64_t rows = T.dw ? q.rows : live;
                 const bool final = q.last && q.slots == 1;
-                int64_t to = -1;
-                float f = 1.f;
-                if (final && row < rows) {
-                    to = q.row_of ? q.row_of[row] : q.row0 + row;
-                    f = q.scale ? *q.scale : 1.f;
+                Emit<OT> emit;
+                if (final) {
+                    int32_t to = -1;
+                    if (row < rows) to = q.row_of ? q.row_of[row] : (int32_t)(q.row0 + row);
+                    emit.rows(to, lane);
                 }
                 const int64_t rb = (int64_t)T.mt * (BM / 32) + (HM / 32) * rank + qd;
 #pragma unroll
@@ -529,8 +540,8 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                         }
                         if (final) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] *= f;
-                            emit(reinterpret_cast<OT*>(q.out), q.ld, p.d, to, col0 + c, v, piece, lane);
+                            for (int i = 0; i < 32; ++i) v[i] *= scale;
+                            emit.put(reinterpret_cast<OT*>(q.out), q.ld, p.d, col0 + c, v, piece, lane);
                         }
                     }
                 }

@@ -47,6 +47,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "rows8.cuh"
 #include "sm100.cuh"
 
 namespace mom {
@@ -104,11 +105,6 @@ struct GemmArgs {
     void* ws;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ void st_shared_v4(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -562,14 +558,20 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                         float mx = m;
 #pragma unroll
                         for (int i = 0; i < 32; ++i) mx = fmaxf(mx, v[i]);
-                        // all -inf so far: exponentials of (-inf - 0) are 0, not NaN
-                        const float sub = mx == -INFINITY ? 0.f : mx * kLog2e;
-                        s *= ex2(fmaf(m, kLog2e, -sub));
+                        // The difference first: exact at the maximum, whose exponential is
+                        // 1 however large it is, and never above 0.  (v log2e - round(mx
+                        // log2e) is off by 2^-24 |mx|: inf for classes masked by -1e10.)
+                        // All -inf so far: exponentials of (-inf - 0) are 0, not NaN.
+                        const float sub = mx == -INFINITY ? 0.f : mx;
+                        const f2 nsub = both(-sub), l2e = both(kLog2e);
+                        s *= fast_ex2((m - sub) * kLog2e);
                         float s2 = 0.f;
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
-                            s += ex2(fmaf(v[i], kLog2e, -sub));
-                            s2 += ex2(fmaf(v[i + 1], kLog2e, -sub));
+                            float e0, e1;
+                            split(mul2(add2(make_f2(v[i], v[i + 1]), nsub), l2e), e0, e1);
+                            s += fast_ex2(e0);
+                            s2 += fast_ex2(e1);
                         }
                         s += s2;
                         m = mx;
@@ -597,7 +599,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                         chunk(c, g);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const float pv = ex2(fmaf(g[i], kLog2e, -lse2));
+                            const float pv = fast_ex2(fmaf(g[i], kLog2e, -lse2));
                             g[i] = c + i < nvr ? wt * (tl == c + i ? pv - 1.f : pv) : 0.f;
                         }
 #pragma unroll
@@ -692,7 +694,7 @@ __global__ void __launch_bounds__(512) join_kernel(const Prod q, const int32_t* 
 __device__ __forceinline__ void lse_join(float& m, float& s, float m2, float s2) {
     if (s2 == 0.f) return;                        // nothing but -inf
     const float mx = fmaxf(m, m2);
-    s = s * (m == mx ? 1.f : ex2((m - mx) * kLog2e)) + s2 * (m2 == mx ? 1.f : ex2((m2 - mx) * kLog2e));
+    s = s * (m == mx ? 1.f : fast_ex2((m - mx) * kLog2e)) + s2 * (m2 == mx ? 1.f : fast_ex2((m2 - mx) * kLog2e));
     m = mx;
 }
 __global__ void __launch_bounds__(1024) logsumexp_kernel(const float2* partials, int n_part, int64_t rows, int64_t row0,

@@ -1,0 +1,87 @@
+"""The vocabulary's cross entropy at the ends of the number range: classes masked
+by finite values, logits far from 0, the largest float32 values and infinities,
+and the parts of a float32 operand.  Against fp64 (oracle/train_ops.py);
+tolerances as in test_gpu_linear_ce.py unless a test derives its own."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import train_ops as T
+from tests.test_gpu_linear_ce import DT, U, _chain, _limits, _np, _problem
+
+pytestmark = pytest.mark.gpu
+
+LOWEST = {"bf16": torch.finfo(torch.bfloat16).min, "f32": torch.finfo(torch.float32).min}
+
+
+def _masked(t, value, at, count, n=70, v=700):
+    """A problem whose classes at .. at + count - 1 have a logit of about
+    `value` for every token: x's first channel is 1 and carries a bias.  Also
+    the kept classes' indices."""
+    d = 72 if t == "bf16" else 65
+    x, w, tg = _problem(n, d, v, t, seed=30)
+    x[:, 0] = 1
+    w[at:at + count, 0] = value
+    keep = torch.ones(v, dtype=torch.bool, device="cuda")
+    keep[at:at + count] = False
+    first = int(keep.nonzero()[0, 0])
+    tg = torch.where((tg >= at) & (tg < at + count), torch.full_like(tg, first), tg)
+    return x, w, tg, keep
+
+
+def _check_masked(x, w, tg, keep, t, gradient=True):
+    """Loss and gradients are those of the kept classes alone; a masked class'
+    probability is 0, so its row of dw is 0 and it adds nothing to dx."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    n = x.shape[0]
+    X, G = _np(x), tg.cpu().numpy()
+    Wk = _np(w[keep])
+    index = (torch.cumsum(keep.int(), 0) - 1).cpu().numpy()
+    Gk = np.where(G >= 0, index[np.where(G >= 0, G, 0)], G)
+    r = np.full(n, 1.0 / (G >= 0).sum())
+    head = LMHead(w)
+    f = head.loss(x, tg)
+    loss, lse, _ = T.linear_ce(X, Wk, Gk)
+    e_lse, e_loss, e_dx, e_dw = _limits(X, Wk, Gk, r, t)
+    assert np.all(np.abs(_np(f["lse"]) - lse) <= e_lse), np.abs(_np(f["lse"]) - lse).max()
+    assert np.all(np.abs(_np(f["loss"]) - loss) <= np.where(G >= 0, e_loss, 0.0))
+    assert np.isfinite(float(f["mean"])) and abs(float(f["mean"]) - loss.sum() * r[0]) <= e_loss.max() + 8 * U
+    if not gradient:
+        return
+    g = head.backward(x, tg)
+    dx, dw, _ = T.linear_ce_grad(X, Wk, Gk, r)
+    half = torch.finfo(DT[t]).eps / 2
+    assert np.all(np.abs(_np(g["dx"]) - dx) <= e_dx + half * np.abs(dx))
+    assert np.all(np.abs(_np(g["dw"][keep]) - dw) <= e_dw + half * np.abs(dw))
+    assert torch.all(g["dw"][~keep] == 0)
+    assert head.device_errors() == {}
+
+
+@pytest.mark.parametrize("at,count", [(0, 40), (128, 128), (300, 32), (320, 64), (660, 40), (0, 650), (50, 650)])
+@pytest.mark.parametrize("t,value", [("bf16", v) for v in (-1e9, -1e10, -1e30, LOWEST["bf16"])] +
+                         [("f32", v) for v in (-1e9, -1e10, -1e30, LOWEST["f32"] / 2)])
+def test_classes_masked_by_finite_values(t, value, at, count):
+    """32 and more neighbouring masked classes: whole chunks, half tiles and
+    tiles that hold nothing else, at the vocabulary's start, inside and end."""
+    _check_masked(*_masked(t, value, at, count), t)
+
+
+@pytest.mark.parametrize("t,value", [(t, v) for t in ("bf16", "f32") for v in (1.0, 2.0 ** 24, 1e10, 1e30, -1e10, -1e30)] +
+                         [("bf16", LOWEST["bf16"]), ("bf16", -LOWEST["bf16"])])
+def test_equal_logits_of_any_size(t, value):
+    _check_equal(t, value)
+
+
+def _check_equal(t, value):
+    """All classes share one logit, whatever its size: lse is that logit plus
+    log v, rounded (twice, and log v's own 2^-21)."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    n, d, v = 40, 64, 700
+    x, w, tg = _problem(n, d, v, t, seed=31)
+    x[:, 0] = 1
+    w.zero_()
+    w[:, 0] = value
+    value = float(w[0, 0])
+    f = LMHead(w).loss(x, tg)
+    want = value + np.log(float(v))
+    assert np.all(np.abs(_np(f["lse"]) - want) <= 2 * U * abs(want) + 2.0 ** -21 * np.log(v))

@@ -841,7 +841,9 @@ mom_status mom_residual_norm_bwd(const void* x, const int8_t* x_codes, const flo
 /* mom_linear_ce_fwd -- softmax cross entropy of the logits z = x w^T, which
  * are never stored: x [n_rows, d], w [vocab, d] (dt), targets [n_rows] int32;
  *   lse[t]  = log(sum_v exp(z[t, v]))
- *   loss[t] = lse[t] - z[t, targets[t]];  0 where targets[t] < 0 (padding)
+ *   loss[t] = lse[t] - z[t, targets[t]];  0 where targets[t] < 0 (padding).
+ *             Formed as (max_v z - z[target]) + log(sum): lse itself holds
+ *             float32's 2^-24 of its size, the loss does not lose that
  *   mean[0] = sum of loss / rows with a target,  mean[1] = 1 / rows with a
  *             target (both 0 when no row has one); mean may be NULL
  * loss, lse [n_rows] float32.  A target >= vocab is recorded in ws

@@ -1,7 +1,8 @@
 // Softmax cross entropy of the logits z = x W^T over a large vocabulary, and
 // its gradient, on the tcgen05 tensor cores without storing the logits.
 //
-//   forward   lse_t = log sum_v exp(z_tv),  loss_t = lse_t - z_t,target
+//   forward   m_t = max_v z_tv,  lse_t = m_t + log sum_v exp(z_tv - m_t),
+//             loss_t = (m_t - z_t,target) + log sum_v exp(z_tv - m_t)
 //   backward  g_tv = exp(z_tv - lse_t) - [v = target_t],
 //             (times the row's weight),  dx = r g W,  dW = r g^T x
 //
@@ -747,10 +748,10 @@ __global__ void __launch_bounds__(1024) logsumexp_kernel(const float2* partials,
         s = sh[0][lane].y;
         float l = 0.f, n = 0.f;
         if (row < rows) {
-            const float ls = m + log2f(s) * kLn2;
+            const float ls0 = log2f(s) * kLn2, ls = m + ls0;
             if (tg >= vocab) record_error(ws, MOM_DEVERR_TARGET, row0 + row);
             if (tg >= 0 && tg < vocab) {
-                l = ls - z;
+                l = (m - z) + ls0;        // not lse - z: far from 0 that keeps 2^-24 of the logits only
                 n = 1.f;
             }
             lse[row] = ls;

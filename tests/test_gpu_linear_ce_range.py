@@ -85,3 +85,54 @@ def _check_equal(t, value):
     f = LMHead(w).loss(x, tg)
     want = value + np.log(float(v))
     assert np.all(np.abs(_np(f["lse"]) - want) <= 2 * U * abs(want) + 2.0 ** -21 * np.log(v))
+
+
+def _integers(t, n=60, d=64, v=700, offset=2 ** 20, seed=32):
+    """x and w of -1, 0 and 1 with a bias of `offset` through x's first channel:
+    every logit and every partial sum of one is an integer below 2^21, exact in
+    float32 under any rounding."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    x = torch.randint(-1, 2, (n, d), generator=g, device="cuda").to(DT[t])
+    w = torch.randint(-1, 2, (v, d), generator=g, device="cuda").to(DT[t])
+    x[:, 0] = 1
+    w[:, 0] = offset
+    tg = torch.randint(0, v, (n,), generator=g, device="cuda", dtype=torch.int32)
+    tg[::7] = -1
+    return x, w, tg
+
+
+@pytest.mark.parametrize("value", [0.0, 2.0 ** 20, -2.0 ** 20])
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_the_loss_keeps_its_digits_far_from_zero(t, value):
+    """loss = (max - z_target) + log(sum): the first term is exact for integer
+    logits, so what is left is the exponentials' and the sum's error, 2^-19,
+    and the rounding of the terms -- not 2^-24 of the logits, 2^-4 here."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    x, w, tg = _integers(t, offset=value)
+    f = LMHead(w).loss(x, tg)
+    G = tg.cpu().numpy()
+    loss, lse, _ = T.linear_ce(_np(x), _np(w), G)
+    lim = 2.0 ** -19 + 8 * U * (np.abs(loss) + np.log(w.shape[0]))
+    assert np.all(np.abs(_np(f["loss"]) - loss) <= lim), np.abs(_np(f["loss"]) - loss).max()
+    assert abs(float(f["mean"]) - loss.sum() / (G >= 0).sum()) <= lim.max()
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_a_sure_prediction_of_a_large_logit(t):
+    """The winning class leads by 8 at a logit of 2^20: the loss is log(1 + ..
+    exp(-8) ..), of the order of 0.2, and the equal logits' loss log v."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    n, d, v = 33, 64, 700
+    x = torch.zeros((n, d), device="cuda").to(DT[t])
+    w = torch.zeros((v, d), device="cuda").to(DT[t])
+    x[:, 0], x[:, 1] = 1, 1
+    w[:, 0] = 2.0 ** 20
+    w[333, 1] = 8
+    tg = torch.full((n,), 333, dtype=torch.int32, device="cuda")
+    f = LMHead(w).loss(x, tg)
+    want = np.log1p((v - 1) * np.exp(-8.0))
+    assert np.all(np.abs(_np(f["loss"]) - want) <= 2.0 ** -19 + 8 * U * np.log(v))
+    w[333, 1] = 0
+    f = LMHead(w).loss(x, tg)
+    assert np.all(np.abs(_np(f["loss"]) - np.log(v)) <= 2.0 ** -19 + 8 * U * np.log(v))

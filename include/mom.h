@@ -861,7 +861,8 @@ mom_status mom_linear_ce_fwd(const void* x, const void* w, const int32_t* target
 /* mom_linear_ce_bwd -- the gradient of sum_t r[t] loss[t], r[t] = dloss[t] *
  * dscale[0] (either NULL: 1; with dscale = mean + 1 of the forward and dloss
  * NULL, of the mean loss), from the forward's lse: with g[t, v] = r[t] (exp(z
- * - lse) - [v = target]), 0 for padding rows,
+ * - lse) - [v = target]), 0 for padding rows (a probability is as exact as
+ * the float32 lse lets it be: 2^-24 |lse|),
  *   dx = g w [n_rows, d],  dw = g^T x [vocab, d]   (dt, overwritten)
  * Padding rows take no part: their x and dloss may hold anything, and they
  * cost nothing but the zeros of their dx.  The logits are formed again in

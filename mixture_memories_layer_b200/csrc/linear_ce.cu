@@ -98,7 +98,7 @@ struct GemmArgs {
     float* zt;                           // the targets' logits
     bf16* g;                             // GRAD: [parts][.., g_pitch], the parts g_part elements apart
     int64_t g_pitch, g_part;
-    const float *lse2, *weight;          // GRAD: log2(e) lse of the packed rows, their weights (null: 1)
+    const float *lse, *weight;           // GRAD: lse of the packed rows, their weights (null: 1)
     int32_t* ticket;                     // STATS: set to 0 for logsumexp_kernel
     // OUT: dx (rows and K of dw follow `live`), dw
     Prod dx, dw;
@@ -454,13 +454,13 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
             const int64_t row = (int64_t)T.mt * BM + HM * rank + 32 * qd + lane;
             const int64_t col0 = (int64_t)T.nt * BN + hf * half;
             int tl = -1;                           // the target's column inside this half tile (< 0: not here)
-            float lse2 = 0.f, wt = 1.f;
+            float lse = 0.f, wt = 1.f;
             if constexpr (EPI != EPI_OUT) {
                 if (row < live) {
                     const int64_t tg = p.targets[row], rel = tg - p.v0 - col0;
                     if (tg >= 0 && tg < p.vocab && rel >= 0 && rel < half) tl = (int)rel;
                     if constexpr (EPI == EPI_GRAD) {
-                        lse2 = p.lse2[row];
+                        lse = p.lse[row];
                         if (p.weight) wt = p.weight[row];
                     }
                 }
@@ -592,6 +592,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                     // shared memory: the MMAs' operands and the copies that bring them
                     // take all of its bandwidth.
                     const int nvr = row < live ? nv : 0;
+                    const f2 nlse = both(-lse);
                     bf16* out = p.g + row * p.g_pitch + col0;
                     const bool some = row < cdiv(live, BK) * BK && row < p.rows;
 #pragma unroll
@@ -599,9 +600,14 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                         float g[32];
                         chunk(c, g);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float pv = fast_ex2(fmaf(g[i], kLog2e, -lse2));
-                            g[i] = c + i < nvr ? wt * (tl == c + i ? pv - 1.f : pv) : 0.f;
+                        for (int i = 0; i < 32; i += 2) {      // (the difference first, as in STATS)
+                            float e[2];
+                            split(mul2(add2(make_f2(g[i], g[i + 1]), nlse), both(kLog2e)), e[0], e[1]);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const float pv = fast_ex2(e[k]);
+                                g[i + k] = c + i + k < nvr ? wt * (tl == c + i + k ? pv - 1.f : pv) : 0.f;
+                            }
                         }
 #pragma unroll
                         for (int part = 0; part < PARTS; ++part) {
@@ -855,7 +861,7 @@ struct GatherArgs {
     int64_t part;                        // elements between the parts
     bf16* xc;                            // the packed rows
     int32_t *targets_c, *row_of, *live;
-    float *lse2, *weight;                // log2(e) lse, dloss
+    float *lse_c, *weight;               // lse, dloss
     void* dx;
     int64_t dx_ld;
     int vec;                             // x, xc and dx take 16-byte accesses
@@ -903,7 +909,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
             if (lane == 0) {
                 a.targets_c[to] = a.targets[row];
                 a.row_of[to] = (int32_t)row;
-                a.lse2[to] = a.lse[row] * kLog2e;
+                a.lse_c[to] = a.lse[row];
                 if (a.dloss) a.weight[to] = a.dloss[row];
             }
             copy_row<T, PARTS>(reinterpret_cast<const T*>(a.x) + row * a.d, a.d, a.xc + to * a.pitch, a.part, a.vec != 0,
@@ -985,7 +991,7 @@ struct Plan {
     int sx, sw;            // K slots of dx and dw
     bool dx_partial, dw_partial;
     bool stage;            // dx and dw leave the GEMM in rows of the pitch (d's are not multiples of 16 bytes)
-    size_t zt, partials, sums, ticket, xbuf, wbuf, g, dxp, dwp, dx_stage, dw_stage, targets, row_of, lse2, weight, live, counts, bytes;
+    size_t zt, partials, sums, ticket, xbuf, wbuf, g, dxp, dwp, dx_stage, dw_stage, targets, row_of, lse_c, weight, live, counts, bytes;
 };
 
 // Columns of the logits' tiles, 256, or 128 where the clusters then finish
@@ -1048,7 +1054,7 @@ Plan plan_for(int64_t n, int d, int64_t v, int dt, bool bwd) {
         if (L.stage && L.sw == 1) L.dw_stage = take((size_t)L.piece * L.pitch * es);
         L.targets = take(n * 4);
         L.row_of = take(n * 4);
-        L.lse2 = take(n * 4);
+        L.lse_c = take(n * 4);
         L.weight = take(n * 4);
         L.live = take(4);
         L.counts = take(cdiv(n, kCountRows) * 4);
@@ -1207,7 +1213,7 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         g.targets_c = i32(L.targets);
         g.row_of = i32(L.row_of);
         g.live = i32(L.live);
-        g.lse2 = f32(L.lse2);
+        g.lse_c = f32(L.lse_c);
         g.weight = f32(L.weight);
         g.dx = dx;
         g.dx_ld = sdx ? L.pitch : a.d;
@@ -1242,7 +1248,7 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         p.g = reinterpret_cast<bf16*>(ws + L.g);
         p.g_pitch = L.piece;
         p.g_part = a.n * L.piece;
-        p.lse2 = f32(L.lse2);
+        p.lse = f32(L.lse_c);
         p.weight = a.dloss ? f32(L.weight) : nullptr;
         p.ws = a.ws;
         MOM_TRY((run_gemm<PARTS, EPI_GRAD>(L.bn_logits, mx_k, mw_k, mx_k, mw_k, p, mt * cdiv(pw, L.bn_logits), true, st)));

@@ -136,3 +136,59 @@ def test_a_sure_prediction_of_a_large_logit(t):
     w[333, 1] = 0
     f = LMHead(w).loss(x, tg)
     assert np.all(np.abs(_np(f["loss"]) - np.log(v)) <= 2.0 ** -19 + 8 * U * np.log(v))
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_the_gradients_exponent_is_a_difference(t):
+    """g = exp(z - lse) - [target] of the lse that is given: with integer logits
+    and an integer lse of 2^20 the exponent is exact, so p has only its own
+    error, 2^-22 of the exponential and 2^-24 of the exponent's |z - lse| log2 e,
+    and g its rounding (bf16, or three parts)."""
+    from mixture_memories_layer_b200 import binding as B
+    x, w, tg = _integers(t, seed=33)
+    n, d = x.shape
+    v = w.shape[0]
+    X, W, G = _np(x), _np(w), tg.cpu().numpy()
+    z = X @ W.T
+    lse = z.max(axis=1) + 3
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    ws = B.new_workspace(B.mom_linear_ce_workspace_size(n, d, v, DT[t], True))
+    r = torch.rand(n, device="cuda") + 0.5
+    B.mom_linear_ce_bwd(x, w, tg, torch.as_tensor(lse, dtype=torch.float32, device="cuda"), r, None, dx, dw, ws)
+    live = G >= 0
+    e = z - lse[:, None]
+    p = np.exp(e) * live[:, None]
+    hot = (np.arange(v)[None, :] == G[:, None]) * live[:, None]
+    R = _np(r)[:, None]
+    g = R * (p - hot)
+    half = torch.finfo(DT[t]).eps / 2
+    dg = np.abs(R) * (p * (2.0 ** -21 + 3 * U * np.abs(e)) + 4 * U * (p + hot)) + (half if t == "bf16" else 2.0 ** -22) * np.abs(g)
+    for got, want, lim in ((dx, g @ W, dg @ np.abs(W) + _chain(v, t) * (np.abs(g) @ np.abs(W))),
+                           (dw, g.T @ X, dg.T @ np.abs(X) + _chain(n, t) * (np.abs(g).T @ np.abs(X)))):
+        assert np.all(np.abs(_np(got) - want) <= lim + half * np.abs(want)), np.abs(_np(got) - want).max()
+
+
+@pytest.mark.parametrize("n,d,v,t", [(70, 72, 700, "bf16"), (300, 65, 9001, "f32"), (2000, 64, 9000, "bf16"), (20, 130, 40001, "bf16")])
+def test_the_gradient_forms_the_losss_logits_again(n, d, v, t):
+    """Logits of 1e10: a class' exponent is 0 (the largest) or below -1000, if the
+    gradient's logit is the one that the loss saw, bit for bit, whatever tiles
+    the two took.  Then g = [largest] - [target], and dx, dw are exact sums of
+    rows (rounded; bf16 weights are 1)."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    x, w, tg = _problem(n, d, v, t, seed=34)
+    w = (w.float() * 1e10).to(DT[t])
+    head = LMHead(w)
+    f = head.loss(x, tg)
+    g = head.backward(x, tg, torch.ones(n, device="cuda"))
+    X, W, G = _np(x), _np(w), tg.cpu().numpy()
+    z = X @ W.T
+    order = np.sort(z, axis=1)
+    sure = order[:, -1] - order[:, -2] > 2e6          # rows whose largest logit leads by many ulps (2^10)
+    assert sure.mean() > 0.9
+    top = z.argmax(axis=1)
+    want = np.where((G >= 0)[:, None], W[top] - W[np.where(G >= 0, G, 0)], 0.0)
+    mag = np.abs(W[top]) + np.abs(W[np.where(G >= 0, G, 0)])
+    lim = torch.finfo(DT[t]).eps / 2 * np.abs(want) + 2.0 ** -21 * mag
+    ok = np.abs(_np(g["dx"]) - want) <= lim
+    assert np.all(ok[sure]) and torch.all(torch.isfinite(g["dx"].float())) and torch.all(torch.isfinite(g["dw"].float()))
+    assert torch.all(torch.isfinite(f["loss"]))

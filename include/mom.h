@@ -851,7 +851,11 @@ mom_status mom_residual_norm_bwd(const void* x, const int8_t* x_codes, const flo
  * and vocab may be any sizes (n_rows and vocab up to 2^30, d up to 2^20, and
  * at most 2^26 tiles of 256 x 128 in dx or dw: MOM_ERR_UNSUPPORTED).  Products
  * are on the bf16 tensor cores with float32 accumulation; float32 operands are
- * split into three bf16 parts.
+ * split into three bf16 parts.  Any finite values may be operands (a logit that
+ * overflows float32 may come out infinite or NaN).  A -inf in w is a masked
+ * class: bf16 takes it as it is (the gradient's 0 * -inf then makes dx NaN),
+ * float32 as the lowest value.  Other infinities and NaN in float32 operands
+ * make the logits they meet NaN.
  * ws: mom_linear_ce_workspace_size(.., backward = 0). */
 size_t mom_linear_ce_workspace_size(int64_t n_rows, int d, int64_t vocab, mom_dtype dt, int backward);
 mom_status mom_linear_ce_fwd(const void* x, const void* w, const int32_t* targets, mom_dtype dt, int64_t n_rows,

@@ -30,8 +30,8 @@
 // an axis so long that one tile would outlast the rest is split into slots
 // that join_kernel adds in order.  No atomics on floats: results repeat.
 //
-// float32 operands: every value is split exactly into three bf16 parts, a =
-// a0 + a1 + a2 (8 bits each), and the six products a_i b_j with i + j <= 2 run
+// float32 operands: every finite value is split exactly into three bf16 parts, a
+// = a0 + a1 + a2 (8 bits each), and the six products a_i b_j with i + j <= 2 run
 // into the same accumulator, smallest first; the rest is below 2^-24 of a
 // product.  The tensor core truncates as it accumulates, so a float32 tile's
 // sum leaves TMEM every 128 of K and is continued in registers, rounded.
@@ -795,10 +795,24 @@ __global__ void __launch_bounds__(1024) logsumexp_kernel(const float2* partials,
     }
 }
 
+// The first part of a float32 value is held to bf16's largest: from 3.396e38 on
+// rounding would make it infinite and the rest of the value NaN.  So every
+// finite value is the sum of its parts; an infinity or a NaN leaves a NaN in
+// the second or third.  W: a -inf (a masked class) counts as the lowest float32
+// value, since products of an infinity with the other operand's parts, of
+// either sign or 0, are no longer its product with that operand.
+template <bool W> __device__ __forceinline__ float split_value(float v) {
+    return W && v == -INFINITY ? -3.402823466e38f : v;
+}
+__device__ __forceinline__ float split_first(float v) {
+    constexpr float big = 3.3895313892515355e38f;      // 0x7f7f
+    return fminf(fmaxf(v, -big), big);
+}
+
 // A row of d elements as its bf16 parts (each `part` elements after the one
 // before) by one warp, several loads in flight.  `vec`: both rows take 16-byte
-// accesses (bf16).
-template <typename T, int PARTS>
+// accesses (bf16); W: a row of W.
+template <typename T, int PARTS, bool W>
 __device__ __forceinline__ void copy_row(const T* __restrict__ src, int d, bf16* __restrict__ dst, int64_t part, bool vec,
                                          int lane) {
     if (PARTS == 1 && vec) {
@@ -821,6 +835,10 @@ __device__ __forceinline__ void copy_row(const T* __restrict__ src, int d, bf16*
             const int c = c0 + 64 * k;
             v[k][0] = c < d ? to_f(src[c]) : 0.f;
             v[k][1] = c + 1 < d ? to_f(src[c + 1]) : 0.f;
+            if constexpr (PARTS > 1) {
+                v[k][0] = split_value<W>(v[k][0]);
+                v[k][1] = split_value<W>(v[k][1]);
+            }
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
@@ -828,7 +846,9 @@ __device__ __forceinline__ void copy_row(const T* __restrict__ src, int d, bf16*
             if (c >= d) break;
 #pragma unroll
             for (int q = 0; q < PARTS; ++q) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(v[k][0], v[k][1]);
+                const bool first = PARTS > 1 && q == 0;
+                const __nv_bfloat162 b = __floats2bfloat162_rn(first ? split_first(v[k][0]) : v[k][0],
+                                                               first ? split_first(v[k][1]) : v[k][1]);
                 *reinterpret_cast<__nv_bfloat162*>(dst + q * part + c) = b;
                 v[k][0] -= __bfloat162float(b.x);
                 v[k][1] -= __bfloat162float(b.y);
@@ -839,12 +859,12 @@ __device__ __forceinline__ void copy_row(const T* __restrict__ src, int d, bf16*
 
 // [rows, d] -> bf16 parts [parts][rows, pitch]: rows that TMA can stride over
 // (a pitch that is a multiple of 8), float32 split into its three parts.
-template <typename T, int PARTS>
+template <typename T, int PARTS, bool W>
 __global__ void __launch_bounds__(256) parts_kernel(const T* src, int64_t rows, int d, int pitch, bf16* dst) {
     after_previous();
     const int64_t step = (int64_t)gridDim.x * 8;
     for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += step)
-        copy_row<T, PARTS>(src + r * d, d, dst + r * pitch, rows * pitch, false, threadIdx.x & 31);
+        copy_row<T, PARTS, W>(src + r * d, d, dst + r * pitch, rows * pitch, false, threadIdx.x & 31);
 }
 
 // The rows that have a target, packed in order.  A block takes 8 rows, one a
@@ -912,8 +932,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
                 a.lse_c[to] = a.lse[row];
                 if (a.dloss) a.weight[to] = a.dloss[row];
             }
-            copy_row<T, PARTS>(reinterpret_cast<const T*>(a.x) + row * a.d, a.d, a.xc + to * a.pitch, a.part, a.vec != 0,
-                               lane);
+            copy_row<T, PARTS, false>(reinterpret_cast<const T*>(a.x) + row * a.d, a.d, a.xc + to * a.pitch, a.part,
+                                      a.vec != 0, lane);
         }
     }
     if (r0 + kGatherRows < a.n) return;
@@ -1102,11 +1122,12 @@ unsigned warps_grid(int64_t warps) {
     return (unsigned)(b < most ? b : most);
 }
 
-cudaError_t to_parts(const void* src, int dt, int64_t rows, int d, int pitch, void* dst, bool next, cudaStream_t st) {
+cudaError_t to_parts(const void* src, int dt, bool w, int64_t rows, int d, int pitch, void* dst, bool next, cudaStream_t st) {
     bf16* o = reinterpret_cast<bf16*>(dst);
     if (dt == MOM_BF16)
-        return launch(parts_kernel<bf16, 1>, warps_grid(rows), 256, 0, next, st, reinterpret_cast<const bf16*>(src), rows, d, pitch, o);
-    return launch(parts_kernel<float, 3>, warps_grid(rows), 256, 0, next, st, reinterpret_cast<const float*>(src), rows, d, pitch, o);
+        return launch(parts_kernel<bf16, 1, false>, warps_grid(rows), 256, 0, next, st, reinterpret_cast<const bf16*>(src), rows, d, pitch, o);
+    return launch(w ? parts_kernel<float, 3, true> : parts_kernel<float, 3, false>, warps_grid(rows), 256, 0, next, st,
+                  reinterpret_cast<const float*>(src), rows, d, pitch, o);
 }
 
 template <typename T>
@@ -1137,7 +1158,7 @@ cudaError_t w_piece(const LinearCeArgs& a, const Plan& L, int64_t v0, int64_t pw
     char* buf = ws_base(a.ws) + L.wbuf;
     w = WPiece{buf, (uint64_t)pw, (uint64_t)L.pitch, 0};
     const size_t es = a.dt == MOM_BF16 ? 2 : 4;
-    return to_parts(reinterpret_cast<const char*>(a.w) + (size_t)v0 * a.d * es, a.dt, pw, a.d, L.pitch, buf, next, st);
+    return to_parts(reinterpret_cast<const char*>(a.w) + (size_t)v0 * a.d * es, a.dt, true, pw, a.d, L.pitch, buf, next, st);
 }
 
 #define MOM_TRY(x) do { const cudaError_t e_ = (x); if (e_ != cudaSuccess) return e_; } while (0)
@@ -1146,7 +1167,7 @@ cudaError_t w_piece(const LinearCeArgs& a, const Plan& L, int64_t v0, int64_t pw
 template <int PARTS> cudaError_t fwd(const LinearCeArgs& a, cudaStream_t st) {
     const Plan L = plan_for(a.n, a.d, a.v, a.dt, false);
     char* ws = ws_base(a.ws);
-    if (!L.direct) MOM_TRY(to_parts(a.x, a.dt, a.n, a.d, L.pitch, ws + L.xbuf, false, st));
+    if (!L.direct) MOM_TRY(to_parts(a.x, a.dt, false, a.n, a.d, L.pitch, ws + L.xbuf, false, st));
     const void* xb = L.direct ? a.x : ws + L.xbuf;
     int n_part = 0;
     float2* partials = reinterpret_cast<float2*>(ws + L.partials);

@@ -192,3 +192,114 @@ def test_the_gradient_forms_the_losss_logits_again(n, d, v, t):
     ok = np.abs(_np(g["dx"]) - want) <= lim
     assert np.all(ok[sure]) and torch.all(torch.isfinite(g["dx"].float())) and torch.all(torch.isfinite(g["dw"].float()))
     assert torch.all(torch.isfinite(f["loss"]))
+
+
+@pytest.mark.parametrize("at,count", [(0, 40), (128, 128), (300, 32), (320, 64), (660, 40), (0, 650), (50, 650)])
+def test_float32_classes_masked_by_the_lowest_value(at, count):
+    _check_masked(*_masked("f32", LOWEST["f32"], at, count), "f32")
+
+
+@pytest.mark.parametrize("value", [LOWEST["f32"], -LOWEST["f32"], 3.391e38])
+def test_float32_logits_of_the_largest_size(value):
+    _check_equal("f32", value)
+
+
+@pytest.mark.parametrize("at,count", [(0, 40), (128, 128), (660, 40), (0, 699), (333, 1)])
+def test_float32_classes_masked_by_minus_infinity(at, count):
+    """A -inf in w counts as the lowest float32 value: in the loss a masked
+    class as in bf16, and in the gradient 0 times a finite number."""
+    x, w, tg, keep = _masked("f32", float("-inf"), at, count)
+    _check_masked(x, w, tg, keep, "f32")
+    # whole rows of -inf, against tokens without a negative channel
+    x = x.abs()
+    w[at:at + count] = float("-inf")
+    _check_masked(x, w, tg, keep, "f32")
+
+
+def test_float32_values_up_to_the_largest():
+    """Values that round to infinity in bf16 are split like any other: in a
+    channel of x that no class uses and in one of w that no token uses they
+    leave logits and the other channels' gradients bit for bit, and their own
+    gradients are 2^100 times those of values 2^100 times smaller (both within
+    a chain of the magnitudes; weights of 1/4 and a class for each token keep
+    the sums finite)."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    n, d, v = 50, 65, 300
+    x, w, tg = _problem(n, d, v, "f32", seed=35, pad=0.0)
+    tg = torch.arange(n, dtype=torch.int32, device="cuda") * 5
+    big = torch.tensor([3.4028234663852886e38, 3.3961775292304957e38, 3.3895313892515355e38, 3.391e38], device="cuda")
+    x[:, 3], w[:, 3], x[:, 7], w[:, 7] = 0, 0, 0, 0
+    x3 = big.repeat(13)[:n] * torch.where(torch.arange(n, device="cuda") % 3 == 0, -1.0, 1.0)
+    w7 = -big.repeat(75)[:v]
+    r = torch.full((n,), 0.25, device="cuda")
+    outs = []
+    for scale in (1.0, 2.0 ** -100):
+        x[:, 3], w[:, 7] = x3 * scale, w7 * scale
+        head = LMHead(w)
+        f = head.loss(x, tg)
+        outs.append({**{k: a.clone() for k, a in f.items()}, **{k: _np(a) for k, a in head.backward(x, tg, r).items()}})
+    a, b = outs
+    assert all(torch.equal(a[k], b[k]) for k in ("loss", "lse", "mean"))
+    other = [c for c in range(d) if c not in (3, 7)]
+    assert np.array_equal(a["dx"][:, other], b["dx"][:, other]) and np.array_equal(a["dw"][:, other], b["dw"][:, other])
+    X, W = _np(x), _np(w)
+    X[:, 3], W[:, 7] = 0, 0
+    g = np.abs(T.linear_ce_grad(X, W, tg.cpu().numpy(), np.full(n, 0.25))[2])
+    for got, want, k, mag in ((a["dw"][:, 3], b["dw"][:, 3], n, g.T @ np.abs(_np(x3))),
+                              (a["dx"][:, 7], b["dx"][:, 7], v, g @ np.abs(_np(w7)))):
+        assert np.all(np.abs(got - want * 2.0 ** 100) <= 2 * _chain(k, "f32") * 1.01 * mag)
+
+
+def test_float32_infinities_and_nan_stay_in_their_rows():
+    """An infinity or a NaN in x makes its row NaN and no other; a +inf in w, or
+    a NaN, every row."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    x, w, tg = _problem(40, 65, 700, "f32", seed=36, pad=0.0)
+    tg[9] = -100
+    clean = LMHead(w).loss(x, tg)["loss"].clone()
+    x2 = x.clone()
+    x2[3, 5], x2[4, 6], x2[5, 7], x2[9, 1] = float("nan"), float("inf"), float("-inf"), float("inf")
+    head = LMHead(w)
+    f = head.loss(x2, tg)
+    rows = [i for i in range(40) if i not in (3, 4, 5, 9)]
+    assert torch.equal(f["loss"][rows], clean[rows]) and f["loss"][9] == 0
+    assert torch.all(torch.isnan(f["loss"][3:6])) and torch.all(torch.isnan(f["lse"][3:6]))
+    g = head.backward(x2, tg, torch.ones(40, device="cuda"))
+    assert torch.all(torch.isfinite(g["dx"][rows])) and torch.all(torch.isnan(g["dx"][3:6])) and torch.all(g["dx"][9] == 0)
+    for bad in (float("inf"), float("nan")):
+        w2 = w.clone()
+        w2[17, 3] = bad
+        assert torch.all(torch.isnan(LMHead(w2).loss(x, tg)["lse"]))
+
+
+def test_float32_parts_hold_every_bit():
+    """One channel and one class: lse is the product x w, of a full mantissa
+    and a power of two, bit for bit.  Two classes with logits of 0: g = -+1/2,
+    and dw and dx repeat all 24 bits of x and w within 1.5 x 2^-20 (p: 2^-22 of
+    the exponential and 2 x 2^-24 of its exponent; six truncated products, 2 x
+    2^-24 each).  Without the third part they would be off by up to 2^-17."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    bits = torch.randint(1 << 23, 1 << 24, (64,), generator=g, device="cuda", dtype=torch.int32) | 1
+    full = bits.float() * 2.0 ** -23 * torch.where(torch.arange(64, device="cuda") % 2 == 0, 1.0, -1.0)
+    zero = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")
+    for k in (0, 5, -30):
+        x, w = torch.zeros((64, 65), device="cuda"), torch.zeros((1, 65), device="cuda")
+        x[:, 40], w[0, 40] = full, 2.0 ** k
+        assert torch.equal(LMHead(w).loss(x, zero(64))["lse"], full * 2.0 ** k)
+        x = torch.zeros((1, 65), device="cuda")
+        for j in range(0, 64, 9):
+            x[0, 40], w[0, 40] = 2.0 ** k, full[j]
+            assert torch.equal(LMHead(w).loss(x, zero(1))["lse"], (full * 2.0 ** k)[j:j + 1])
+    lim = 1.5 * 2.0 ** -20 * full.abs()
+    head = LMHead(torch.zeros((2, 64), device="cuda"))
+    x = full[None].clone()
+    head.loss(x, zero(1))
+    dw = head.backward(x, zero(1))["dw"]
+    assert torch.all((dw[0] + full / 2).abs() <= lim) and torch.all((dw[1] - full / 2).abs() <= lim)
+    head = LMHead(torch.stack([full, torch.zeros_like(full)]))
+    x = torch.zeros((1, 64), device="cuda")
+    head.loss(x, zero(1))
+    dx = head.backward(x, zero(1))["dx"]
+    assert torch.all((dx[0] + full / 2).abs() <= lim)

@@ -868,6 +868,7 @@ mom_status mom_linear_ce_fwd(const void* x, const void* w, const int32_t* target
  * - lse) - [v = target]), 0 for padding rows (a probability is as exact as
  * the float32 lse lets it be: 2^-24 |lse|),
  *   dx = g w [n_rows, d],  dw = g^T x [vocab, d]   (dt, overwritten)
+ * A target >= vocab is recorded in ws (MOM_DEVERR_TARGET) and counts as padding.
  * Padding rows take no part: their x and dloss may hold anything, and they
  * cost nothing but the zeros of their dx.  The logits are formed again in
  * pieces of the vocabulary and g, without dscale, is held for one piece at a

@@ -885,6 +885,7 @@ struct GatherArgs {
     void* dx;
     int64_t dx_ld;
     int vec;                             // x, xc and dx take 16-byte accesses
+    void* ws;
 };
 __device__ __forceinline__ bool has_target(int32_t t, int64_t vocab) { return t >= 0 && t < vocab; }
 __device__ __forceinline__ int block_sum(int v) {
@@ -921,6 +922,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
     const int64_t to = before + __popc(in & ((1u << warp) - 1u));
     if (row < a.n) {
         if (!((in >> warp) & 1u)) {                // dx of padding is 0
+            if (lane == 0 && a.targets[row] >= 0) record_error(a.ws, MOM_DEVERR_TARGET, row);      // (>= vocab)
             T* o = reinterpret_cast<T*>(a.dx) + row * a.dx_ld;
             const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (a.vec) for (int c = lane * 8; c < a.d; c += 256) store_vec<8>(o + c, z);
@@ -1239,6 +1241,7 @@ template <int PARTS> cudaError_t bwd(const LinearCeArgs& a, cudaStream_t st) {
         g.dx = dx;
         g.dx_ld = sdx ? L.pitch : a.d;
         g.vec = a.d % 8 == 0;
+        g.ws = a.ws;
         if (a.n > kCountRows) {
             MOM_TRY(launch(count_kernel, cdiv(a.n, kCountRows), 256, 0, false, st, a.targets, a.n, a.v, i32(L.counts)));
         }

@@ -303,3 +303,23 @@ def test_float32_parts_hold_every_bit():
     head.loss(x, zero(1))
     dx = head.backward(x, zero(1))["dx"]
     assert torch.all((dx[0] + full / 2).abs() <= lim)
+
+
+def test_a_target_beyond_the_vocabulary_is_recorded_in_the_gradient():
+    """The gradient's own workspace keeps the violation too, and the row counts
+    as padding."""
+    from mixture_memories_layer_b200 import binding as B
+    for t, n, row in (("bf16", 50, 7), ("f32", 20, 19), ("bf16", 20000, 17001)):
+        x, w, tg = _problem(n, 64, 300, t, seed=37)
+        tg[row] = 300 + row
+        lse = torch.full((n,), 5.0, device="cuda")
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        ws = B.new_workspace(B.mom_linear_ce_workspace_size(n, 64, 300, DT[t], True))
+        B.mom_linear_ce_bwd(x, w, tg, lse, None, None, dx, dw, ws)
+        assert B.mom_get_error(ws) == (B.MOM_DEVERR_TARGET, row)
+        assert torch.all(dx[row] == 0)
+        tg[row] = -100
+        dx2, dw2 = torch.empty_like(x), torch.empty_like(w)
+        ws = B.new_workspace(B.mom_linear_ce_workspace_size(n, 64, 300, DT[t], True))
+        B.mom_linear_ce_bwd(x, w, tg, lse, None, None, dx2, dw2, ws)
+        assert B.mom_get_error(ws) == (0, 0) and torch.equal(dx, dx2) and torch.equal(dw, dw2)

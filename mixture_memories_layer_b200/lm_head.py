@@ -46,10 +46,7 @@ class LMHead:
             b = self._bufs["bwd", n] = (new(n), self._bufs["dw"], size)
         return b
 
-    def _workspace(self, name, nbytes, stream):
-        if stream is not None:
-            with torch.cuda.stream(stream):
-                return self._workspace(name, nbytes, None)
+    def _workspace(self, name, nbytes):
         t = self._ws.get(name)
         if t is None or t.numel() < nbytes:
             t = self._ws[name] = B.new_workspace(nbytes, self.device)
@@ -61,8 +58,11 @@ class LMHead:
         """x [N, d_model], targets [N] int32 (negative: padding).  Returns
         ``loss`` [N] (0 for padding), ``lse`` [N], the ``mean`` loss over the
         rows with a target and ``inv_count`` = 1 / their number (0-d)."""
+        if stream is not None:      # buffers that a first call makes belong to its stream
+            with torch.cuda.stream(stream):
+                return self.loss(x, targets)
         loss, lse, both, mean, inv_count, _, size = self._fwd_bufs(x.shape[0])
-        B.mom_linear_ce_fwd(x, self.w, targets, loss, lse, both, self._workspace("fwd", size, stream), stream=stream)
+        B.mom_linear_ce_fwd(x, self.w, targets, loss, lse, both, self._workspace("fwd", size))
         return dict(loss=loss, lse=lse, mean=mean, inv_count=inv_count)
 
     def backward(self, x: torch.Tensor, targets: torch.Tensor, dloss: Optional[torch.Tensor] = None,
@@ -71,13 +71,16 @@ class LMHead:
         is read): ``dx`` [N, d_model] and ``dw`` [vocab, d_model] in the
         weight's type, of the mean loss, or with dloss [N] float32 of
         sum(dloss * loss)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(x, targets, dloss)
         n = x.shape[0]
         fwd = self._bufs.get(("fwd", n))
         if fwd is None:
             raise ValueError("backward follows a loss call of the same shape")
         dx, dw, size = self._bwd_bufs(n)
         B.mom_linear_ce_bwd(x, self.w, targets, fwd[1], dloss, None if dloss is not None else fwd[5], dx, dw,
-                            self._workspace("bwd", size, stream), stream=stream)
+                            self._workspace("bwd", size))
         return dict(dx=dx, dw=dw)
 
     def device_errors(self):

@@ -69,9 +69,12 @@ class MoMStack:
         [N, d_model] in the blocks' type).  Returns ``h`` [N, d_model], the
         normed output, and ``x``, the stream after the last block (both
         written again by the next call); x itself is left as it is."""
+        if stream is not None:      # buffers that a first call makes, the blocks' too, belong to its stream
+            with torch.cuda.stream(stream):
+                return self.forward(x, cu_seqlens, gates)
         self._check_gates(gates)
         n = x.shape[0]
-        st = stream if stream is not None else torch.cuda.current_stream()
+        st = torch.cuda.current_stream(self.device)
         h = self._buf("h", (n, self.d_model), self.dtype)
         out = self._buf("x", (n, self.d_model), self.stream_dtype)
         B.mom_residual_norm(x, None, None, None, None, self.norms[0]["w_pre"], self.eps, None, h, stream=st)
@@ -92,16 +95,18 @@ class MoMStack:
         float32, the gradient of the input stream, ``dw_final`` and ``levels``:
         for each block dw_pre, dw_post, dres_scale, dgate (where it has them)
         and ``block``, the block's own gradients (MoMBlock.backward)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(cu_seqlens, dh, dx, gates)
         self._check_gates(gates)
         n = dh.shape[0]
-        st = stream if stream is not None else torch.cuda.current_stream()
+        st = torch.cuda.current_stream(self.device)
         f32 = torch.float32
         g = self._buf("dx", (n, self.d_model), f32)
         ws = self._bufs.get(("ws", n))
         if ws is None:
-            with torch.cuda.stream(st):
-                ws = self._bufs[("ws", n)] = B.new_workspace(B.mom_residual_norm_bwd_workspace_size(n, self.d_model),
-                                                             self.device)
+            ws = self._bufs[("ws", n)] = B.new_workspace(B.mom_residual_norm_bwd_workspace_size(n, self.d_model),
+                                                         self.device)
         levels: List[Dict] = [None] * len(self.blocks)
         vec = lambda name, i: self._buf("%s%d" % (name, i), (self.d_model,), f32)
         dw_next = vec("dw_final", 0)
@@ -135,9 +140,12 @@ class MoMStack:
         """One token a sequence: x [B, d_model] (stream_dtype); states: for
         each block (state, conv_sh, conv_mem) of MoMBlock.decode_step, updated
         in place.  Returns ``h`` and ``x`` as forward."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.decode_step(x, states, gates)
         self._check_gates(gates)
         n = x.shape[0]
-        st = stream if stream is not None else torch.cuda.current_stream()
+        st = torch.cuda.current_stream(self.device)
         h = self._buf("dec_h", (n, self.d_model), self.dtype)
         out = self._buf("dec_x", (n, self.d_model), self.stream_dtype)
         B.mom_residual_norm(x, None, None, None, None, self.norms[0]["w_pre"], self.eps, None, h, stream=st)

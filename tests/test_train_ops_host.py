@@ -1,0 +1,103 @@
+"""What MoMStack and LMHead do on the host, without a GPU: the library's calls
+are replaced by records of their arguments (CPU)."""
+import contextlib
+
+import pytest
+import torch
+
+N, D, V = 6, 8, 10
+
+
+class Stream:
+    cuda_stream = 77
+
+    def __init__(self, name):
+        self.name = name
+
+
+class Recorder:
+    """Which stream was current as each buffer was made and each call launched."""
+
+    def __init__(self, monkeypatch):
+        from mixture_memories_layer_b200 import binding as B
+        self.default, self.calls, self.made = Stream("default"), [], []
+        self.current = self.default
+
+        @contextlib.contextmanager
+        def stream(s):
+            before, self.current = self.current, s
+            yield
+            self.current = before
+        monkeypatch.setattr(torch.cuda, "stream", stream)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.current)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+        for name in ("empty", "zeros"):
+            make = getattr(torch, name)
+            monkeypatch.setattr(torch, name, lambda *a, make=make, **k: (self.made.append(self.current), make(*a, **k))[1])
+        for name in ("mom_linear_ce_fwd", "mom_linear_ce_bwd", "mom_residual_norm", "mom_residual_norm_bwd"):
+            monkeypatch.setattr(B, name, lambda *a, name=name, stream=None, **k:
+                                self.calls.append((name, stream or self.current, a, k)))
+
+
+class Block:
+    """A block that keeps its buffers as MoMBlock does."""
+
+    def __init__(self, rec, d_model=D, dtype=torch.bfloat16):
+        self.rec, self.d_model, self.dtype, self.device, self.made = rec, d_model, dtype, torch.device("cpu"), {}
+
+    def block_buffers(self, n, n_seq):
+        if n not in self.made:
+            self.made[n] = torch.empty((n, self.d_model), dtype=self.dtype)
+        return dict(y=self.made[n])
+
+    def forward(self, x, cu, stream=None):
+        self.rec.calls.append(("block", stream, (x,), {}))
+        return self.block_buffers(x.shape[0], cu.numel() - 1)
+
+    def backward(self, x, cu, dy, stream=None):
+        self.rec.calls.append(("block_bwd", stream, (x,), {}))
+        return dict(dx=torch.empty(x.shape, dtype=torch.float32))
+
+    def decode_step(self, x, stream=None):
+        self.rec.calls.append(("block_dec", stream, (x,), {}))
+        return self.block_buffers(x.shape[0], 1)["y"], None
+
+
+@pytest.fixture
+def rec(monkeypatch):
+    from mixture_memories_layer_b200 import build
+    build.build(verbose=False)
+    return Recorder(monkeypatch)
+
+
+def _stack(rec, levels=2, **kw):
+    from mixture_memories_layer_b200.residual import MoMStack
+    w = torch.ones(D)
+    return MoMStack([Block(rec) for _ in range(levels)], [dict(w_pre=w, w_post=w) for _ in range(levels)], w, **kw)
+
+
+def _cu(*ends):
+    return torch.tensor((0,) + ends, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_buffers_are_made_on_the_stream_that_uses_them(rec, side):
+    """The caching allocator hands memory out in the order of the stream that it
+    is made on: a buffer made on the current stream and written on another one
+    could still be in use by a kernel queued on the first."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    head, stack = LMHead(torch.zeros((V, D))), _stack(rec)
+    x, tg = torch.zeros((N, D)), torch.zeros(N, dtype=torch.int32)
+    xs, dh = torch.zeros((N, D), dtype=torch.bfloat16), torch.zeros((N, D))
+    rec.made.clear()
+    s = Stream("side") if side else None
+    head.loss(x, tg, stream=s)
+    head.backward(x, tg, stream=s)
+    head.backward(x, tg, torch.ones(N), stream=s)
+    stack.forward(xs, _cu(2, N), stream=s)
+    stack.backward(_cu(2, N), dh, stream=s)
+    stack.decode_step(xs, [(), ()], stream=s)
+    want = s or rec.default
+    assert len(rec.made) > 20 and all(m is want for m in rec.made)
+    assert len(rec.calls) > 15 and all(c[1] is want for c in rec.calls)
+    assert rec.current is rec.default

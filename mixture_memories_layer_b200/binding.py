@@ -663,6 +663,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
+def current_stream_id(device):
+    """What tells a device's current stream from its others."""
+    return _raw_stream(device.index if device.index is not None else _current_device())
+
+
 def _launch(what, fn, dev, stream, *args):
     """fn(*args, stream) on device `dev`; stream None: that device's current one."""
     if dev < 0:

@@ -25,7 +25,7 @@ class LMHead:
         self.w = weight
         self.vocab, self.d_model = weight.shape
         self.dtype, self.device = weight.dtype, weight.device
-        self._bufs, self._ws, self._held = {}, {}, []
+        self._bufs, self._ws, self._made_on, self._held = {}, {}, {}, []
 
     def _fwd_bufs(self, n):
         b = self._bufs.get(("fwd", n))
@@ -50,6 +50,10 @@ class LMHead:
         t = self._ws.get(name)
         if t is None or t.numel() < nbytes:
             t = self._ws[name] = B.new_workspace(nbytes, self.device)
+            self._made_on[name] = B.current_stream_id(self.device)
+        elif B.current_stream_id(self.device) != self._made_on[name]:
+            # freed when a larger one takes its place, but not before this stream is done with it
+            t.record_stream(torch.cuda.current_stream(self.device))
         if torch.cuda.is_current_stream_capturing() and not any(t is h for h in self._held):
             self._held.append(t)    # a graph keeps its workspace when a larger one takes its place
         return t

@@ -31,6 +31,7 @@ class Recorder:
         monkeypatch.setattr(torch.cuda, "stream", stream)
         monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.current)
         monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+        monkeypatch.setattr(B, "current_stream_id", lambda device: self.current.name)
         for name in ("empty", "zeros"):
             make = getattr(torch, name)
             monkeypatch.setattr(torch, name, lambda *a, make=make, **k: (self.made.append(self.current), make(*a, **k))[1])
@@ -101,3 +102,37 @@ def test_buffers_are_made_on_the_stream_that_uses_them(rec, side):
     assert len(rec.made) > 20 and all(m is want for m in rec.made)
     assert len(rec.calls) > 15 and all(c[1] is want for c in rec.calls)
     assert rec.current is rec.default
+
+
+def test_a_workspace_outlives_the_streams_that_use_it(rec, monkeypatch):
+    """A workspace that a larger one replaces goes back to the allocator, which
+    must know every stream that used it besides the one that it was made on."""
+    from mixture_memories_layer_b200 import binding as B
+    from mixture_memories_layer_b200.lm_head import LMHead
+
+    class Workspace:
+        def __init__(self, nbytes):
+            self.nbytes, self.used_on = nbytes, []
+
+        def numel(self):
+            return self.nbytes
+
+        def record_stream(self, stream):
+            self.used_on.append(stream.name)
+    made = []
+    monkeypatch.setattr(B, "new_workspace", lambda nbytes, device=None: (made.append(Workspace(nbytes)), made[-1])[1])
+    head = LMHead(torch.zeros((V, D)))
+    x, tg = torch.zeros((N, D)), torch.zeros(N, dtype=torch.int32)
+    a, b = Stream("a"), Stream("b")
+    head.loss(x, tg, stream=a)
+    head.loss(x, tg, stream=a)
+    assert len(made) == 1 and made[0].used_on == []
+    head.loss(x, tg, stream=b)
+    head.loss(x, tg)
+    assert len(made) == 1 and set(made[0].used_on) == {"b", "default"}
+    n = 100000
+    head.loss(torch.zeros((n, D)), torch.zeros(n, dtype=torch.int32), stream=b)
+    head.loss(x, tg, stream=b)
+    assert len(made) == 2 and made[1].used_on == []
+    head.loss(x, tg, stream=a)
+    assert made[1].used_on == ["a"]

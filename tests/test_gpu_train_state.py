@@ -53,3 +53,44 @@ def test_a_stack_on_a_side_stream():
         s.synchronize()
         _same({**_flat(out), **_flat(grads, "g")}, want)
         torch.cuda.synchronize()
+
+
+def _tokens(n, d, v, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    x = torch.randn((n, d), generator=g, device="cuda").to(BF)
+    return x, torch.randint(-20, v, (n,), generator=g, device="cuda", dtype=torch.int32)
+
+
+@pytest.mark.parametrize("capture", [False, True])
+def test_a_gradient_after_an_evaluation_of_the_same_size(capture):
+    """A loss kept by the caller gives the same gradients when other losses of
+    the same number of rows came between; without it they are the last one's."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    x, tg = _tokens(130, 64, 500, 1)
+    x2, tg2 = _tokens(130, 64, 500, 2)
+    w = _tokens(500, 64, 1, 3)[0]
+    ref = LMHead(w)
+    want_loss = _flat(ref.loss(x, tg))
+    want = _flat(ref.backward(x, tg))
+    head = LMHead(w)
+    keep = head.new_loss(130)
+    torch.cuda.synchronize()
+
+    def step():
+        head.loss(x, tg, out=keep)
+        head.loss(x2, tg2)
+        return head.backward(x, tg, saved=keep)
+    got = step()
+    if capture:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = step()
+        for t in (*keep.values(), *got.values()):
+            t.zero_()
+        graph.replay()
+    assert all(torch.equal(want_loss["." + k], keep[k]) for k in ("loss", "lse", "mean", "inv_count"))
+    assert all(torch.equal(want["." + k], got[k]) for k in got)
+    assert not torch.equal(head.backward(x, tg)["dx"], want[".dx"])
+    head.loss(x, tg)
+    assert torch.equal(head.backward(x, tg)["dx"], want[".dx"])

@@ -136,3 +136,27 @@ def test_a_workspace_outlives_the_streams_that_use_it(rec, monkeypatch):
     assert len(made) == 2 and made[1].used_on == []
     head.loss(x, tg, stream=a)
     assert made[1].used_on == ["a"]
+
+
+def test_the_heads_own_and_the_callers_outputs(rec):
+    """What a call reads and writes: the head's own tensors, one set a number of
+    rows and one dw, or the caller's."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    head = LMHead(torch.zeros((V, D)))
+    x, tg = torch.zeros((N, D)), torch.zeros(N, dtype=torch.int32)
+    with pytest.raises(ValueError, match="loss"):
+        head.backward(x, tg)
+    own = head.loss(x, tg)
+    assert head.loss(x, tg)["lse"] is own["lse"] and head.loss(x[:2], tg[:2])["lse"] is not own["lse"]
+    keep = head.new_loss(N)
+    assert head.loss(x, tg, out=keep) is keep
+    _, _, a, _ = rec.calls[-1]
+    assert a[3] is keep["loss"] and a[4] is keep["lse"] and a[5] is keep["mean_inv"]
+    assert keep["mean"].data_ptr() == a[5].data_ptr() and keep["inv_count"].data_ptr() == a[5].data_ptr() + 4
+    g = head.backward(x, tg)
+    _, _, a, _ = rec.calls[-1]
+    assert a[3] is own["lse"] and a[5].data_ptr() == own["inv_count"].data_ptr() and a[7] is g["dw"]
+    head.backward(x, tg, saved=keep)
+    _, _, a, _ = rec.calls[-1]
+    assert a[3] is keep["lse"] and a[5].data_ptr() == keep["inv_count"].data_ptr() and tuple(a[5].shape) == (1,)
+    LMHead(torch.zeros((V, D))).backward(x, tg, saved=keep)      # no loss call of its own is needed

@@ -16,8 +16,9 @@ from . import binding as B
 class LMHead:
     """weight [vocab, d_model], bf16 or float32.  Outputs and workspaces are
     made once and written again: loss, lse, mean, inv_count and dx by the next
-    call with the same number of rows, dw by the next backward.  A caller who
-    needs a loss longer gives tensors of its own (out, saved below).  Every number of rows keeps its outputs as long as the head lives.
+    call with the same number of rows, dw by the next backward of any number.
+    A caller who needs them longer gives tensors of its own (out, saved, dw
+    below).  Every number of rows keeps its outputs as long as the head lives.
     Calls of one head must not overlap on the GPU."""
 
     def __init__(self, weight: torch.Tensor):
@@ -86,17 +87,19 @@ class LMHead:
         return out if out is not None else dict(loss=loss, lse=lse, mean=mean, inv_count=inv_count)
 
     def backward(self, x: torch.Tensor, targets: torch.Tensor, dloss: Optional[torch.Tensor] = None, stream=None,
-                 saved: Optional[Dict[str, torch.Tensor]] = None) -> Dict[str, torch.Tensor]:
+                 saved: Optional[Dict[str, torch.Tensor]] = None,
+                 dw: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
         """Gradients for a loss on the same x and targets, whose lse and
         inv_count are read: from ``saved``, what loss(.., out=) wrote, or else
         from this head's last loss call with N rows -- which must have been that
         one: where another loss of N rows, an evaluation say, comes between the
         two, give ``saved``.  ``dx`` [N, d_model] and ``dw`` [vocab, d_model]
         in the weight's type, of the mean loss, or with dloss [N] float32 of
-        sum(dloss * loss)."""
+        sum(dloss * loss); dw into the tensor given, or else into the head's one
+        (overwritten by every backward)."""
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.backward(x, targets, dloss, saved=saved)
+                return self.backward(x, targets, dloss, saved=saved, dw=dw)
         n = x.shape[0]
         if saved is not None:
             lse, inv_count = saved["lse"], saved["inv_count"].view(1)
@@ -106,7 +109,8 @@ class LMHead:
                 raise ValueError("backward follows a loss call of the same shape")
             lse, inv_count = fwd[1], fwd[5]
         dx, size = self._bwd_bufs(n)
-        dw = self._dw()
+        if dw is None:
+            dw = self._dw()
         B.mom_linear_ce_bwd(x, self.w, targets, lse, dloss, None if dloss is not None else inv_count, dx, dw,
                             self._workspace("bwd", size))
         return dict(dx=dx, dw=dw)

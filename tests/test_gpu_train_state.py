@@ -94,3 +94,31 @@ def test_a_gradient_after_an_evaluation_of_the_same_size(capture):
     assert not torch.equal(head.backward(x, tg)["dx"], want[".dx"])
     head.loss(x, tg)
     assert torch.equal(head.backward(x, tg)["dx"], want[".dx"])
+
+
+def test_weight_gradients_of_two_micro_batches():
+    """dw is the head's one buffer, whatever the number of rows; a tensor of the
+    caller's is left alone by the next call."""
+    from mixture_memories_layer_b200.lm_head import LMHead
+    w = _tokens(500, 64, 1, 3)[0]
+    a, b = _tokens(100, 64, 500, 4), _tokens(200, 64, 500, 5)
+    alone = []
+    for x, tg in (a, b):
+        h = LMHead(w)
+        h.loss(x, tg)
+        alone.append(h.backward(x, tg)["dw"].clone())
+    head = LMHead(w)
+    mine = [torch.full_like(w, 7.0) for _ in range(2)]
+    for (x, tg), dw in zip((a, b), mine):
+        head.loss(x, tg)
+        assert head.backward(x, tg, dw=dw)["dw"] is dw
+    assert all(torch.equal(x, y) for x, y in zip(mine, alone))
+    g = []
+    for x, tg in (a, b):
+        head.loss(x, tg)
+        g.append(head.backward(x, tg))
+    assert g[0]["dw"] is g[1]["dw"] and torch.equal(g[1]["dw"], alone[1])
+    assert torch.equal(mine[0], alone[0])
+    for bad in (w[:-1], w.float(), torch.empty((64, 500), dtype=BF, device="cuda").t()):
+        with pytest.raises(ValueError, match="dw"):
+            head.backward(*a, dw=bad)

@@ -156,7 +156,11 @@ def test_the_heads_own_and_the_callers_outputs(rec):
     g = head.backward(x, tg)
     _, _, a, _ = rec.calls[-1]
     assert a[3] is own["lse"] and a[5].data_ptr() == own["inv_count"].data_ptr() and a[7] is g["dw"]
-    head.backward(x, tg, saved=keep)
+    mine = torch.zeros((V, D))
+    g2 = head.backward(x, tg, saved=keep, dw=mine)
     _, _, a, _ = rec.calls[-1]
     assert a[3] is keep["lse"] and a[5].data_ptr() == keep["inv_count"].data_ptr() and tuple(a[5].shape) == (1,)
-    LMHead(torch.zeros((V, D))).backward(x, tg, saved=keep)      # no loss call of its own is needed
+    assert a[7] is mine and g2["dw"] is mine and g2["dx"] is g["dx"]
+    assert head.backward(x[:2], tg[:2])["dw"] is g["dw"]      # one dw, whatever the number of rows
+    other = LMHead(torch.zeros((V, D)))
+    assert other.backward(x, tg, saved=keep, dw=mine)["dw"] is mine      # no loss call of its own is needed

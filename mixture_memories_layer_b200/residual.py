@@ -41,6 +41,7 @@ class MoMStack:
         if any(b.d_model != self.d_model for b in blocks):
             raise ValueError("the blocks' d_model differ")
         self._bufs = {}
+        self._ran = None            # what the last forward was given (None: none, or not to its end)
 
     def _buf(self, name, shape, dtype):
         key = (name, tuple(shape), dtype)
@@ -57,6 +58,12 @@ class MoMStack:
     def _check_gates(self, gates):
         if gates is not None and len(gates) != len(self.blocks):
             raise ValueError("gates has %d entries for %d blocks" % (len(gates), len(self.blocks)))
+
+    def _given(self, n, cu_seqlens, gates):
+        """What a backward has to share with the forward just run: the numbers
+        of rows and sequences, and each level's kind of gate."""
+        kinds = [g if g is None else "token" if g.numel() == n else "element" for g in gates or [None] * len(self.blocks)]
+        return n, cu_seqlens.numel() - 1, kinds
 
     def _w_next(self, i):
         return self.norms[i + 1]["w_pre"] if i + 1 < len(self.blocks) else self.w_final
@@ -75,6 +82,7 @@ class MoMStack:
         self._check_gates(gates)
         n = x.shape[0]
         st = torch.cuda.current_stream(self.device)
+        self._ran = None
         h = self._buf("h", (n, self.d_model), self.dtype)
         out = self._buf("x", (n, self.d_model), self.stream_dtype)
         B.mom_residual_norm(x, None, None, None, None, self.norms[0]["w_pre"], self.eps, None, h, stream=st)
@@ -84,6 +92,7 @@ class MoMStack:
             B.mom_residual_norm(x, y, gates[i] if gates else None, w["w_post"], w.get("res_scale"), self._w_next(i),
                                 self.eps, out, h, pack=self._k8(i, n), stream=st)
             x = out
+        self._ran = self._given(n, cu_seqlens, gates)
         return dict(h=h, x=out)
 
     # ------------------------------------------------------------- backward
@@ -91,7 +100,8 @@ class MoMStack:
                  gates: Optional[List] = None, stream=None) -> Dict:
         """Gradients of <dh, h> + <dx, x> for the forward just run with the
         same cu_seqlens and gates (its checkpoints and the blocks' buffers are
-        read; dh, dx [N, d_model] float32).  Returns ``dx`` [N, d_model]
+        read, which the next forward of any size overwrites; dh, dx [N,
+        d_model] float32).  Returns ``dx`` [N, d_model]
         float32, the gradient of the input stream, ``dw_final`` and ``levels``:
         for each block dw_pre, dw_post, dres_scale, dgate (where it has them)
         and ``block``, the block's own gradients (MoMBlock.backward)."""
@@ -100,6 +110,9 @@ class MoMStack:
                 return self.backward(cu_seqlens, dh, dx, gates)
         self._check_gates(gates)
         n = dh.shape[0]
+        if self._ran != self._given(n, cu_seqlens, gates):
+            raise ValueError("backward of %d rows in %d sequences: the forward just run must have had the same, and the "
+                             "same kinds of gates" % (n, cu_seqlens.numel() - 1))
         st = torch.cuda.current_stream(self.device)
         f32 = torch.float32
         g = self._buf("dx", (n, self.d_model), f32)

@@ -122,3 +122,25 @@ def test_weight_gradients_of_two_micro_batches():
     for bad in (w[:-1], w.float(), torch.empty((64, 500), dtype=BF, device="cuda").t()):
         with pytest.raises(ValueError, match="dw"):
             head.backward(*a, dw=bad)
+
+
+def test_a_stack_refuses_another_batchs_backward():
+    """A forward of another size in between (the blocks' routing tables are its
+    own now); the right order gives what the sizes give alone."""
+    w, _, _, _, _, stack, _ = _build(2, 81)
+    x, cu, dh, gate = _batch(w, (40, 25), 7)
+    x2, cu2, dh2, gate2 = _batch(w, (30, 9), 8)
+    alone = []
+    for a in ((x, cu, dh, gate), (x2, cu2, dh2, gate2)):
+        fresh = _build(2, 81)[5]
+        fresh.forward(a[0], a[1], [a[3], None])
+        alone.append(_flat(fresh.backward(a[1], a[2], gates=[a[3], None])))
+    with pytest.raises(ValueError, match="forward"):
+        stack.backward(cu, dh, gates=[gate, None])
+    stack.forward(x, cu, [gate, None])
+    stack.forward(x2, cu2, [gate2, None])
+    with pytest.raises(ValueError, match="forward"):
+        stack.backward(cu, dh, gates=[gate, None])
+    _same(_flat(stack.backward(cu2, dh2, gates=[gate2, None])), alone[1])
+    stack.forward(x, cu, [gate, None])
+    _same(_flat(stack.backward(cu, dh, gates=[gate, None])), alone[0])

@@ -164,3 +164,36 @@ def test_the_heads_own_and_the_callers_outputs(rec):
     assert head.backward(x[:2], tg[:2])["dw"] is g["dw"]      # one dw, whatever the number of rows
     other = LMHead(torch.zeros((V, D)))
     assert other.backward(x, tg, saved=keep, dw=mine)["dw"] is mine      # no loss call of its own is needed
+
+
+def test_a_stack_refuses_a_backward_without_its_forward(rec):
+    """Its checkpoints and the blocks' buffers would be uninitialised, or those
+    of another batch."""
+    stack = _stack(rec)
+    xs, dh = torch.zeros((N, D), dtype=torch.bfloat16), torch.zeros((N, D))
+    tok, el = torch.zeros((N, 1), dtype=torch.bfloat16), torch.zeros((N, D), dtype=torch.bfloat16)
+
+    def refused(*a, **k):
+        before = len(rec.calls)
+        with pytest.raises(ValueError, match="forward"):
+            stack.backward(*a, **k)
+        assert len(rec.calls) == before
+    refused(_cu(2, N), dh)                                        # none yet
+    stack.forward(xs, _cu(2, N), [tok, None])
+    refused(_cu(2, 4), dh[:4], gates=[tok[:4], None])             # other rows
+    refused(_cu(2, 3, N), dh, gates=[tok, None])                  # other sequences
+    for gates in (None, [None, None], [None, tok], [el, None], [tok, tok]):
+        refused(_cu(2, N), dh, gates=gates)
+    stack.backward(_cu(2, N), dh, gates=[tok[:, 0], None])        # a token's gate may be [N] or [N, 1]
+    stack.backward(_cu(2, N), dh, gates=[tok, None])              # again, from the same forward
+    stack.decode_step(xs[:3], [(), ()])
+    stack.backward(_cu(2, N), dh, gates=[tok, None])              # decoding leaves what it reads
+    stack.forward(xs[:4], _cu(1, 4))
+    refused(_cu(2, N), dh, gates=[tok, None])                     # the blocks' routing tables are the last forward's
+    stack.backward(_cu(1, 4), dh[:4])
+    stack.forward(xs, _cu(3, 4, N), [tok, None])
+    refused(_cu(2, N), dh, gates=[tok, None])                     # overwritten since
+    stack.blocks[1].forward = lambda *a, **k: 1 / 0
+    with pytest.raises(ZeroDivisionError):
+        stack.forward(xs, _cu(3, 4, N), [tok, None])
+    refused(_cu(3, 4, N), dh, gates=[tok, None])                  # not to its end

@@ -40,6 +40,8 @@ class MoMStack:
         self.d_model, self.device = blocks[0].d_model, blocks[0].device
         if any(b.d_model != self.d_model for b in blocks):
             raise ValueError("the blocks' d_model differ")
+        if any(b.dtype != self.dtype for b in blocks):
+            raise ValueError("the blocks are of different types")
         self._bufs = {}
         self._ran = None            # what the last forward was given (None: none, or not to its end)
 

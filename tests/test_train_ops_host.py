@@ -197,3 +197,12 @@ def test_a_stack_refuses_a_backward_without_its_forward(rec):
     with pytest.raises(ZeroDivisionError):
         stack.forward(xs, _cu(3, 4, N), [tok, None])
     refused(_cu(3, 4, N), dh, gates=[tok, None])                  # not to its end
+
+
+def test_a_stack_refuses_blocks_of_two_types(rec):
+    from mixture_memories_layer_b200.residual import MoMStack
+    w = dict(w_pre=torch.ones(D), w_post=torch.ones(D))
+    with pytest.raises(ValueError, match="type"):
+        MoMStack([Block(rec), Block(rec, dtype=torch.float32)], [w, w], torch.ones(D))
+    with pytest.raises(ValueError, match="d_model"):
+        MoMStack([Block(rec), Block(rec, d_model=2 * D)], [w, w], torch.ones(D))

@@ -144,3 +144,48 @@ def test_a_stack_refuses_another_batchs_backward():
     _same(_flat(stack.backward(cu2, dh2, gates=[gate2, None])), alone[1])
     stack.forward(x, cu, [gate, None])
     _same(_flat(stack.backward(cu, dh, gates=[gate, None])), alone[0])
+
+
+@pytest.mark.parametrize("stream_dtype", [BF, torch.float32])
+def test_a_stack_that_keeps_its_stream_in_its_own_type(stream_dtype):
+    """The forward's bits are those with 8-bit checkpoints; the gradients at the
+    first block are those of the norm's adjoint on the input itself, bit for
+    bit, and no longer those on a restored one."""
+    from mixture_memories_layer_b200 import binding as B
+    from mixture_memories_layer_b200.residual import MoMStack
+    w, _, _, _, _, stack, _ = _build(2, 91, stream_dtype)
+    plain = MoMStack(_build(2, 91)[5].blocks, stack.norms, stack.w_final, stack.eps, stream_dtype, act8=False)
+    x, cu, dh, gate = _batch(w, (50, 3, 33), 9)
+    x = x.to(stream_dtype) + (0.001 if stream_dtype == torch.float32 else 0)
+    keep = x.clone()
+    gates = [gate, None]
+    want = _flat(stack.forward(x, cu, gates))
+    quant = _flat(stack.backward(cu, dh, gates=gates))
+    n, d = x.shape
+    one = MoMStack(plain.blocks[:1], plain.norms[:1], plain.w_final, plain.eps, stream_dtype, act8=False)
+    one.forward(x, cu, [gate])
+    y = one.blocks[0].block_buffers(n, 3)["y"]
+    vec = lambda: torch.empty(d, device="cuda")
+    dx, dy, dgate, dwp, dsc, dwf = torch.empty_like(dh), torch.empty_like(y), torch.empty_like(gate), vec(), vec(), vec()
+    ws = B.new_workspace(B.mom_residual_norm_bwd_workspace_size(n, d))
+    nm = one.norms[0]
+    B.mom_residual_norm_bwd(keep, y, gate, nm["w_post"], nm["res_scale"], one.w_final, one.eps, None, dh, dx, dy, dgate,
+                            dwp, dsc, dwf, ws)
+    x.zero_()                                  # the stack has its own copy
+    g = one.backward(cu, dh, gates=[gate])
+    lev = g["levels"][0]
+    assert torch.equal(g["dw_final"], dwf) and torch.equal(lev["dw_post"], dwp)
+    assert torch.equal(lev["dres_scale"], dsc) and torch.equal(lev["dgate"], dgate)
+    x.copy_(keep)
+    got = _flat(plain.forward(x, cu, gates))
+    assert all(torch.equal(got[k], want[k]) for k in want) and torch.equal(x, keep)
+    x.zero_()
+    exact = _flat(plain.backward(cu, dh, gates=gates))
+    assert exact.keys() == quant.keys()
+    # 8 bits: half a code is 1/254 of a group's largest; the gradients differ, by less than a tenth
+    for k in (".dx", ".dw_final", ".levels.0.dw_pre", ".levels.1.dw_post"):
+        r = float((exact[k] - quant[k]).norm() / exact[k].norm())
+        assert 0 < r < 0.1, (k, r)
+    x.copy_(keep)
+    _same(_flat(plain.forward(x, cu, gates)), want)
+    _same(_flat(plain.backward(cu, dh, gates=gates)), exact)

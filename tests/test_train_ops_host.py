@@ -206,3 +206,30 @@ def test_a_stack_refuses_blocks_of_two_types(rec):
         MoMStack([Block(rec), Block(rec, dtype=torch.float32)], [w, w], torch.ones(D))
     with pytest.raises(ValueError, match="d_model"):
         MoMStack([Block(rec), Block(rec, d_model=2 * D)], [w, w], torch.ones(D))
+
+
+@pytest.mark.parametrize("act8", [True, False])
+def test_what_a_stack_keeps_for_its_backward(rec, act8):
+    """8-bit checkpoints, or the stream itself in buffers of each level's own
+    (the caller's input is copied: it may be overwritten after the forward)."""
+    stack = _stack(rec, 3, act8=act8)
+    x = torch.zeros((N, D), dtype=torch.bfloat16)
+    out = stack.forward(x, _cu(N))
+    fwd = [c[2:] for c in rec.calls if c[0] == "mom_residual_norm"]
+    rec.calls.clear()
+    stack.backward(_cu(N), torch.zeros((N, D)))
+    bwd = [c[2][0] for c in rec.calls if c[0] == "mom_residual_norm_bwd"]
+    restored = [c[2][0] for c in rec.calls if c[0] == "mom_residual_norm"]
+    assert fwd[0][0][0] is x and len(fwd) == 4 and len(bwd) == 4 and len(restored) == 3
+    if act8:
+        codes = [k["pack"][0] for _, k in fwd[1:]]
+        assert all(c is b[0] for c, b in zip(codes, reversed(bwd[:3]))) and all(c is r[0] for c, r in zip(codes, reversed(restored)))
+        assert bwd[3][0] is bwd[2][0] and len({id(b[0]) for b in bwd}) == 3
+        assert all(b[0].dtype == torch.int8 for b in bwd)
+    else:
+        ins, outs = [a[0] for a, _ in fwd], [a[7] for a, _ in fwd]
+        assert all(k.get("pack") is None for _, k in fwd)
+        assert all(i is o for i, o in zip(ins[1:], outs)) and len({id(o) for o in outs}) == 4
+        assert all(b is o for b, o in zip(reversed(bwd[:3]), outs)) and bwd[3] is outs[0]
+        assert all(r is o for r, o in zip(reversed(restored), outs))
+        assert out["x"] is outs[3]

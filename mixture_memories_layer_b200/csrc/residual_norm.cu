@@ -50,8 +50,10 @@ template <bool VEC> struct RawX<Q8, VEC> : Raw8Q<VEC> {
 };
 
 // sigma(z) = 1 / (1 + e), e = exp(-z), by the hardware exponential and
-// reciprocal: below 2^-21 relative for |z| < 8 (2^-18 at |z| = 60, where sigma
-// or 1 - sigma is 1e-26).  1 - sigma without cancellation: e sigma for z > 0.
+// reciprocal.  Its relative error is at most 1.22 |z| + 4 + 1 + 2 in 2^-24: the
+// exponent's two roundings, the exponential, the sum, the reciprocal; 2^-19.9
+// for |z| < 8, 2^-17.6 at 60, where sigma or 1 - sigma is 1e-26.  1 - sigma
+// without cancellation: e sigma for z > 0.
 __device__ __forceinline__ float sigmoid(float z, float& rest) {
     const float e = fast_ex2(z * -1.4426950408889634f), s = fast_rcp(1.f + e);
     rest = z > 0.f ? e * s : 1.f - s;

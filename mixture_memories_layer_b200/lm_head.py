@@ -82,6 +82,8 @@ class LMHead:
                 return self.loss(x, targets, out=out)
         loss, lse, both, mean, inv_count, _, size = self._fwd_bufs(x.shape[0])
         if out is not None:
+            if "mean_inv" not in out:
+                raise ValueError("out is a dict that new_loss made")
             loss, lse, both = out["loss"], out["lse"], out["mean_inv"]
         B.mom_linear_ce_fwd(x, self.w, targets, loss, lse, both, self._workspace("fwd", size))
         return out if out is not None else dict(loss=loss, lse=lse, mean=mean, inv_count=inv_count)

@@ -148,6 +148,8 @@ def test_the_heads_own_and_the_callers_outputs(rec):
         head.backward(x, tg)
     own = head.loss(x, tg)
     assert head.loss(x, tg)["lse"] is own["lse"] and head.loss(x[:2], tg[:2])["lse"] is not own["lse"]
+    with pytest.raises(ValueError, match="new_loss"):
+        head.loss(x, tg, out=own)
     keep = head.new_loss(N)
     assert head.loss(x, tg, out=keep) is keep
     _, _, a, _ = rec.calls[-1]

@@ -547,18 +547,33 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                 const int nv = left < 0 ? 0 : left < half ? (int)left : half;      // valid columns of the half tile
                 if constexpr (EPI == EPI_STATS) {
                     float m = -INFINITY, s = 0.f, zt = 0.f;
+                    // 64 columns at a time where registers allow it, two loads in flight
+                    // (16384 rows, d 64, 8000 classes: 62 us, 66 with 32)
+                    constexpr int CW = SEG ? 32 : 64;
 #pragma unroll
-                    for (int c = 0; c < half; c += 32) {
-                        float v[32];
-                        chunk(c, v);
-                        if (c + 32 > nv) {
+                    for (int c = 0; c < half; c += CW) {
+                        float v[CW];
+                        if constexpr (SEG) {
+                            chunk(c, v);
+                        } else {
+                            uint32_t r0[32], r1[32];
+                            tmem_ld_x32(taddr + c, r0);
+                            tmem_ld_x32(taddr + c + 32, r1);
+                            tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
+                            for (int i = 0; i < 32; ++i) {
+                                v[i] = __uint_as_float(r0[i]);
+                                v[32 + i] = __uint_as_float(r1[i]);
+                            }
+                        }
+                        if (c + CW > nv) {
+#pragma unroll
+                            for (int i = 0; i < CW; ++i)
                                 if (c + i >= nv) v[i] = -INFINITY;
                         }
                         float mx = m;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, v[i]);
+                        for (int i = 0; i < CW; ++i) mx = fmaxf(mx, v[i]);
                         // The difference first: exact at the maximum, whose exponential is
                         // 1 however large it is, and never above 0.  (v log2e - round(mx
                         // log2e) is off by 2^-24 |mx|: inf for classes masked by -1e10.)
@@ -568,7 +583,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                         s *= fast_ex2((m - sub) * kLog2e);
                         float s2 = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
+                        for (int i = 0; i < CW; i += 2) {
                             float e0, e1;
                             split(mul2(add2(make_f2(v[i], v[i + 1]), nsub), l2e), e0, e1);
                             s += fast_ex2(e0);
@@ -576,9 +591,9 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                         }
                         s += s2;
                         m = mx;
-                        if (tl >= c && tl < c + 32) {
+                        if (tl >= c && tl < c + CW) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
+                            for (int i = 0; i < CW; ++i)
                                 if (tl == c + i) zt = v[i];
                         }
                     }

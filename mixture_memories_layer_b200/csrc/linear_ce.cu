@@ -196,8 +196,9 @@ struct Tile {
 // the longer tiles first, round robin; the clusters that got one fewer take
 // the head start of as many of the other's tiles as last as long as one, and
 // the rest goes round robin, those clusters first.  Closed form, so that every
-// role walks the same list, in 32 bits: 64-bit divisions for each tile cost 1-3 %
-// (2047 tokens of 65003 classes: 900 us, 880 us without).
+// role walks the same list, in 32 bits: 64-bit divisions for each tile cost 2-3 %
+// (a call by itself: 2047 tokens, d 1024, 65003 classes 738 us, 722 without; 4096
+// tokens, d 64, 30000 classes 237 and 230).
 struct Schedule {
     uint32_t c, n, m1, m2, n_tiles, na, nb, head, first, own;
     int kb1, kb2, k1, k2, dw_first;
@@ -603,9 +604,9 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                     }
                 } else {
                     // g is 0 past the vocabulary and past the packed rows, up to whole
-                    // K blocks of dW (or n, past which TMA fills in zeros).  A lane writes its row in 32-byte sectors, past
-                    // shared memory: the MMAs' operands and the copies that bring them
-                    // take all of its bandwidth.
+                    // K blocks of dW (or n, past which TMA fills in zeros).  A lane
+                    // writes its row in 32-byte sectors, past shared memory: the MMAs'
+                    // operands and the copies that bring them take all of its bandwidth.
                     const int nvr = row < live ? nv : 0;
                     const f2 nlse = both(-lse);
                     bf16* out = p.g + row * p.g_pitch + col0;
@@ -1033,8 +1034,8 @@ struct Plan {
 
 // Columns of the logits' tiles, 256, or 128 where the clusters then finish
 // first: by the instructions' cycles (512 for 256 columns of a K block) and
-// 1500 for a tile's rest.  200 tokens of 8000 classes, d 360, float32: 121 us
-// with 256 (32 tiles for 74 clusters), 88 us with 128.
+// 1500 for a tile's rest.  200 tokens of 8000 classes, d 360, float32: 95 us
+// with 256 (32 tiles for 74 clusters), 82 us with 128.
 int columns_for(int64_t rows, int64_t cols, int d, int parts, int clusters) {
     const int64_t kb = cdiv(d, BK) * (parts == 1 ? 1 : 6), m = cdiv(rows, BM);
     auto cost = [&](int bn) { return cdiv(m * cdiv(cols, bn), clusters) * (kb * 2 * bn + 1500); };
@@ -1066,8 +1067,11 @@ Plan plan_for(int64_t n, int d, int64_t v, int dt, bool bwd) {
         L.ticket = take(4);
     } else {
         // 128 columns where 256 would leave a quarter or more of them empty;
-        // float32, whose six products need fewer bytes each, a tenth (1001 x
-        // 515 x 8009: 248 us, 254 us with 256)
+        // float32, whose six products need fewer bytes each, a tenth.  float32,
+        // 256 -> 128 columns, us: 1001 x 515 x 8009 244 -> 240, 1001 x 1100 x
+        // 8009 387 -> 377, 4000 x 1100 x 4000 701 -> 643.  Below a tenth it goes
+        // either way: 1001 x 1300 x 8009 459 -> 451, 4000 x 1300 x 4000 775 ->
+        // 786, 200 x 1660 x 16000 356 -> 364.
         const int64_t narrow = up(d, 128), wide = up(d, 256);
         L.bn = (b16 ? narrow * 4 <= wide * 3 : narrow * 11 < wide * 10) ? 128 : 256;
         L.bn_logits = columns_for(n, L.piece < v ? L.piece : v, d, L.parts, clusters);

@@ -11,14 +11,14 @@
 //   dgate = D s w_post n_y sigma (1 - sigma)        (its row's sum for one gate a token)
 //   A    = sum_t D sigma n_y,  dw_post = s A,  ds = w_post A,  dw_pre = sum_t dh n_x
 //
-// Bound by memory, and nearly as much by issuing instructions (65 % of the
-// issue slots with 16 warps an SM).  A row is spread over the W warps of a CTA,
-// C chunks of 256 channels a warp; every operand is read from memory once and
-// later rows' operands are on their way while one is worked on.  Sums, norms
-// and the whole arithmetic are float32; each output is rounded once, as it is
-// stored.  16384 x 1024 bf16 with an element gate: forward 35 us, 4.8 TB/s;
-// adjoint with float32 gradients and the stream from its checkpoint 73 us, 4.8
-// TB/s (a plain copy of 4 GB: 6.6).
+// Bound by memory and, with the 16 warps an SM that the registers leave, by each
+// warp's own latencies (56 % of the issue slots forward, 62 % in the adjoint).
+// A row is spread over the W warps of a CTA, C chunks of 256 channels a warp;
+// every operand is read from memory once and later rows' operands are on their
+// way while one is worked on.  Sums, norms and the whole arithmetic are float32;
+// each output is rounded once, as it is stored.  16384 x 1024 bf16 with an
+// element gate: forward 35 us, 4.8 TB/s; adjoint with float32 gradients and the
+// stream from its checkpoint 72 us, 4.9 TB/s (a plain copy of 4 GB: 6.6).
 #include <type_traits>
 
 #include "rows8.cuh"
